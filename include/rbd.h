@@ -431,9 +431,107 @@ rbd_status rbd_svdquant_fit(const void* w, int64_t N, int64_t K, rbd_qcfg cfg, i
                             int32_t iters, const double* omegas, const double* act_rms, void* q, float* scales,
                             double* l1, double* l2, double* errs, int32_t* best, void* work, void* stream);
 
+/* ---- 8-bit paged key/value cache --------------------------------------------
+ * Keys and values of many sequences in pages of 64 tokens, one byte a value,
+ * with one float32 scale per (page, head, side); attention that reads it, and
+ * eviction by the weight attention gave every key.  Beside the INT4 ring codec,
+ * whose reads go back to bf16 first.  Heads are 128 channels wide.
+ *
+ *   codes   uint8 [pages, heads, 2, 64, 128], 16-byte aligned; side 0 keys,
+ *           side 1 values.  The value of (token t of the page, channel d) is the
+ *           byte at 128 t + 16 ((d / 16) xor (t mod 8)) + d mod 16 of its
+ *           [64, 128] tile, an int8 or an E4M3 value by code_format.
+ *   scales  float32 [pages, heads, 2], 8-byte aligned; value = code * scale.
+ *   table   int32 [seqs, ldt] (device): page of tokens 64 p .. 64 p + 63 of
+ *           every sequence; the first max_pages columns are used.
+ *   lens    int32 [seqs] (device): tokens held, at most 64 max_pages.
+ *   cu      int32 [seqs + 1] (device): sequence b has rows cu[b] .. cu[b+1] - 1
+ *           of the packed tensors of a call.  Rows of no sequence are neither
+ *           read nor written.
+ * Offsets, lengths and page indices on the device are checked by the kernels:
+ * what lies outside its buffer is skipped and rbd_check reports
+ * RBD_ERR_INVALID_ARG.  Page indices repeated among the pages a call writes are
+ * a race (of values, never of bounds).  Limits: heads <= 1024, seqs <= 65535.  */
+typedef struct rbd_kv8 {
+  uint8_t* codes;
+  float* scales;
+  const int32_t* table;
+  int64_t ldt;
+  int64_t pages;
+  int64_t max_pages;
+  int64_t seqs;
+  int32_t heads;
+  int32_t code_format;   /* rbd_code_format */
+} rbd_kv8;
+
+/* Append: tokens lens[b] .. lens[b] + n - 1 of sequence b from its n rows of
+ * k, v (bf16 [rows, ld], head h at h * 128; ld >= 128 heads, ld % 8 == 0,
+ * 16-byte aligned).  lens is not changed.  Per (page, head, side), float32:
+ *   s = max(s_old, RN(amax / qmax), 2^-100), code = round(RN(x * RN(1 / s))),
+ * qmax 127 (INT8: nearest whole number, ties to even, within -127 .. 127) or 448
+ * (E4M3: nearest value, ties to even, saturating); amax over the finite new
+ * values of the page; s_old the page's scale if it held tokens, whose codes are
+ * formed again from RN(code * s_old) when the scale grows.  NaN is stored as 0,
+ * an infinity as the largest code.  Appending the same rows at the same lens
+ * twice changes nothing the second time.                                      */
+rbd_status rbd_kv8_append(const rbd_kv8* cache, const int32_t* lens, const int32_t* cu, const void* k, int64_t ldk,
+                          const void* v, int64_t ldv, int64_t rows, void* stream);
+
+/* Read: the last `tokens` tokens of every sequence as RN_bf16(code * scale) into
+ * k, v (bf16 [seqs * tokens, ld]); rows before a sequence's first token are zero.
+ * seqs * tokens * heads <= 2^37.                                              */
+rbd_status rbd_kv8_read(const rbd_kv8* cache, const int32_t* lens, int64_t tokens, void* k, int64_t ldk, void* v,
+                        int64_t ldv, void* stream);
+
+/* Bytes of device scratch rbd_kv8_attn needs (weigh: with weights); -1 for bad
+ * sizes.                                                                      */
+int64_t rbd_kv8_attn_workspace_bytes(int64_t seqs, int64_t heads, int64_t q_heads, int64_t rows, int64_t max_len,
+                                     int32_t weigh);
+
+/* Attention: o = softmax(q k^T * softmax_scale) v over the lens[b] tokens held.
+ *   q, o    bf16 [rows, ld], q_heads heads of 128 channels a row; query head j
+ *           reads cache head j / (q_heads / heads); ld % 8 == 0, 16-byte aligned.
+ *   causal  nonzero: the n queries of a sequence are its last n tokens, query i
+ *           sees tokens 0 .. lens[b] - n + i; zero: every query sees all tokens.
+ *           A query that sees no token gets zeros.
+ *   max_len at least every lens[b] (a longer one is refused on the device); the
+ *           launch is laid out for it, so that a captured call stays right for
+ *           any lengths up to it.
+ *   weights_in, weights_out  both NULL, or float32 with element (b, h, t) at
+ *           b * w_seq + h * w_head + t, w_head >= max_len: weights_out = weights_in +
+ *           the sum, over the queries of sequence b and the query heads of cache
+ *           head h, of the weight key t got; t < lens[b] only.  They may be the same.
+ *   work    rbd_kv8_attn_workspace_bytes(...) bytes, 256-byte aligned (NULL if 0).
+ * Scores, softmax statistics and sums are float32 on exact products of codes and
+ * queries; the softmax's numerators are rounded to fp16 for the second product.
+ * No result depends on timing.  rows * q_heads <= 2^30.                       */
+rbd_status rbd_kv8_attn(const rbd_kv8* cache, const int32_t* lens, const int32_t* cu, const void* q, int64_t ldq,
+                        int64_t rows, int64_t q_heads, int32_t causal, float softmax_scale, int64_t max_len, void* o,
+                        int64_t ldo, const float* weights_in, float* weights_out, int64_t w_seq, int64_t w_head,
+                        void* work, int64_t work_bytes, void* stream);
+
+/* Eviction: every (sequence, head) keeps at most `keep` tokens, its last `recent`
+ * ones and, of those in front, the ones of largest weight (equal weights: the
+ * earlier token; a NaN ranks lowest), in their order.
+ *   weights     float32, element (b, h, t) at b * w_seq + h * w_head + t, width columns
+ *               (w_head >= width); lens[b] <= width.
+ *   dst_table   int32 [seqs, ld_dst], ld_dst >= ceil(keep / 64): pages that take the
+ *               kept tokens (quantised as by append from code * scale).  None may be
+ *               a page the sequences hold.
+ *   kept        int32 [seqs, heads, keep]: positions kept, ascending, then -1.
+ *   weights_out float32 (strides o_seq, o_head; width_out >= keep columns): the kept
+ *               tokens' weights, then zeros; may be `weights`.
+ *   lens_out    int32 [seqs]: min(lens, keep); not `lens` itself.
+ * 0 <= recent <= keep, keep >= 1.                                             */
+rbd_status rbd_kv8_evict(const rbd_kv8* cache, const int32_t* lens, const float* weights, int64_t w_seq,
+                         int64_t w_head, int64_t width, int64_t keep, int64_t recent, const int32_t* dst_table,
+                         int64_t ld_dst, int32_t* kept, float* weights_out, int64_t o_seq, int64_t o_head,
+                         int64_t width_out, int32_t* lens_out, void* stream);
+
 /* Synchronises `stream`, then reports the first device-side error recorded
- * since the last rbd_check (RBD_ERR_DEVICE_TIMEOUT) or a CUDA error, and
- * clears the device status word.                                              */
+ * since the last rbd_check (RBD_ERR_DEVICE_TIMEOUT, or RBD_ERR_INVALID_ARG for
+ * device-side metadata a paged-cache kernel refused) or a CUDA error, and
+ * clears the device status words.                                             */
 rbd_status rbd_check(void* stream);
 
 /* Launches a single-thread kernel that waits on an mbarrier nobody signals,

@@ -37,8 +37,13 @@ from ._binding import (  # noqa: F401
     rbd_attn_workspace_bytes,
     rbd_attn_quant,
     rbd_attn_int8,
+    rbd_kv8_append,
+    rbd_kv8_read,
+    rbd_kv8_attn_workspace_bytes,
+    rbd_kv8_attn,
+    rbd_kv8_evict,
     rbd_svdquant_fit,
 )
 from .attention import attention_operands, int8_attention  # noqa: F401
-from .kvcache import Int4KVCache  # noqa: F401
+from .kvcache import Int4KVCache, Int8KVCache  # noqa: F401
 from .layer import RotatedLowBitLinear  # noqa: F401

@@ -22,6 +22,7 @@ STATUS_NAMES = {0: "RBD_OK", 1: "RBD_ERR_INVALID_ARG", 2: "RBD_ERR_UNSUPPORTED",
 EXPORTED = ("rbd_rot_quant_act", "rbd_norm_rot_quant_act", "rbd_lowrank_fused", "rbd_lowrank_down", "rbd_pack_weights_int4", "rbd_pack_weights_int8",
             "rbd_w4a4_linear", "rbd_w8a8_linear", "rbd_nvfp4_scale_bytes", "rbd_nvfp4_quant",
             "rbd_nvfp4_quant_noalloc", "rbd_nvfp4_linear", "rbd_kv4_encode", "rbd_kv4_decode", "rbd_qk_norm_rope", "rbd_rope_tables", "rbd_attn_workspace_bytes", "rbd_attn_quant", "rbd_attn_int8",
+            "rbd_kv8_append", "rbd_kv8_read", "rbd_kv8_attn_workspace_bytes", "rbd_kv8_attn", "rbd_kv8_evict",
             "rbd_svdquant_workspace_bytes", "rbd_svdquant_fit",
             "rbd_check", "rbd_debug_timeout_probe", "rbd_status_string", "rbd_version")
 
@@ -46,6 +47,13 @@ class Epilogue(ctypes.Structure):
                 ("r", ctypes.c_int32), ("gate_mode", ctypes.c_int32), ("gate_col0", ctypes.c_int64),
                 ("gate_col1", ctypes.c_int64), ("gate", ctypes.c_void_p), ("residual", ctypes.c_void_p),
                 ("ldr", ctypes.c_int64), ("acc_debug", ctypes.c_void_p)]
+
+
+class Kv8(ctypes.Structure):
+    """rbd_kv8: the buffers of an 8-bit paged key/value cache."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("ldt", ctypes.c_int64), ("pages", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("seqs", ctypes.c_int64), ("heads", ctypes.c_int32), ("code_format", ctypes.c_int32)]
 
 
 _LIB = None
@@ -85,6 +93,11 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "rbd_rope_tables": [vp, i64, ctypes.c_double, vp, vp, vp],
         "rbd_attn_quant": [vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp, vp],
         "rbd_attn_int8": [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp],
+        "rbd_kv8_append": [ctypes.POINTER(Kv8), vp, vp, vp, i64, vp, i64, i64, vp],
+        "rbd_kv8_read": [ctypes.POINTER(Kv8), vp, i64, vp, i64, vp, i64, vp],
+        "rbd_kv8_attn": [ctypes.POINTER(Kv8), vp, vp, vp, i64, i64, i64, i32, ctypes.c_float, i64, vp, i64, vp, vp, i64,
+                         i64, vp, i64, vp],
+        "rbd_kv8_evict": [ctypes.POINTER(Kv8), vp, vp, i64, i64, i64, i64, i64, vp, i64, vp, vp, i64, i64, i64, vp, vp],
         "rbd_svdquant_fit": [vp, i64, i64, QCfg, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
         "rbd_check": [vp],
         "rbd_debug_timeout_probe": [i64, vp],
@@ -97,6 +110,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.rbd_nvfp4_scale_bytes.restype = i64
     lib.rbd_attn_workspace_bytes.argtypes = [i64, i64]
     lib.rbd_attn_workspace_bytes.restype = i64
+    lib.rbd_kv8_attn_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i32]
+    lib.rbd_kv8_attn_workspace_bytes.restype = i64
     lib.rbd_svdquant_workspace_bytes.argtypes = [i64, i64, i32, i32, QCfg]
     lib.rbd_svdquant_workspace_bytes.restype = i64
     lib.rbd_status_string.argtypes = [ctypes.c_int]
@@ -368,6 +383,123 @@ def rbd_attn_int8(qc: torch.Tensor, sq: torch.Tensor, kc: torch.Tensor, sk: torc
     Tk = kc.shape[1]
     _ok(load().rbd_attn_int8(_ptr(qc), _ptr(sq), _ptr(kc), _ptr(sk), _ptr(vt), Tq, Tk, H, sk.shape[1], _ptr(o),
                              _rowstride(o), _stream(stream)), "rbd_attn_int8")
+
+
+def _kv8(table: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, code_format: int) -> Kv8:
+    """The rbd_kv8 of table int32 [seqs, pages per sequence], codes uint8 [pages, heads, 2, 64, 128] and
+    scales float32 [pages, heads, 2]."""
+    if codes.dtype != torch.uint8 or codes.dim() != 5 or tuple(codes.shape[2:]) != (2, 64, 128) or \
+            not codes.is_contiguous():
+        raise ValueError("codes must be contiguous uint8 [pages, heads, 2, 64, 128]")
+    if scales.dtype != torch.float32 or tuple(scales.shape) != (codes.shape[0], codes.shape[1], 2) or \
+            not scales.is_contiguous():
+        raise ValueError("scales must be contiguous float32 [pages, heads, 2]")
+    if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be row-major int32 [seqs, pages per sequence]")
+    ldt = table.stride(0) if table.shape[0] > 1 else table.shape[1]
+    return Kv8(_ptr(codes), _ptr(scales), _ptr(table), ldt, codes.shape[0], table.shape[1], table.shape[0],
+               codes.shape[1], code_format)
+
+
+def _i32(t: torch.Tensor, shape, what: str):
+    """Device address of a contiguous int32 tensor of the given shape."""
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
+    return _ptr(t)
+
+
+def _bf16_rows(t: torch.Tensor, cols: int, what: str) -> int:
+    """Row stride of bf16 [rows, >= cols]."""
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] < cols:
+        raise ValueError(f"{what} must be bf16 [rows, >= {cols}]")
+    return _rowstride(t) if t.shape[0] > 1 else max(t.stride(0), cols)
+
+
+def _weights(t: torch.Tensor, seqs: int, heads: int, what: str):
+    """(sequence stride, head stride, columns) of float32 [seqs, heads, columns]."""
+    if t.dtype != torch.float32 or t.dim() != 3 or t.shape[0] != seqs or t.shape[1] != heads or \
+            (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be float32 [{seqs}, {heads}, columns] with adjacent columns")
+    return t.stride(0), (t.stride(1) if heads > 1 else max(t.stride(1), t.shape[2])), t.shape[2]
+
+
+def rbd_kv8_append(k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                   codes: torch.Tensor, scales: torch.Tensor, code_format: int = CODES_INT8, stream=None) -> None:
+    """k, v bf16 [rows, >= heads*128] -> tokens lens[b] .. of every sequence b, whose rows are cu[b] ..
+    cu[b+1] - 1 (cu int32 [seqs + 1], lens int32 [seqs]; lens is not changed)."""
+    c = _kv8(table, codes, scales, code_format)
+    cols = c.heads * 128
+    ldk, ldv = _bf16_rows(k, cols, "k"), _bf16_rows(v, cols, "v")
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v differ in rows")
+    _ok(load().rbd_kv8_append(ctypes.byref(c), _i32(lens, (c.seqs,), "lens"), _i32(cu, (c.seqs + 1,), "cu"), _ptr(k),
+                              ldk, _ptr(v), ldv, k.shape[0], _stream(stream)), "rbd_kv8_append")
+
+
+def rbd_kv8_read(lens: torch.Tensor, table: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, k: torch.Tensor,
+                 v: torch.Tensor, code_format: int = CODES_INT8, stream=None) -> None:
+    """The last T tokens of every sequence -> k, v bf16 [seqs, T, heads*128] (contiguous; zeros in front of a
+    sequence's first token)."""
+    c = _kv8(table, codes, scales, code_format)
+    for t in (k, v):
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != c.seqs or t.shape[2] != c.heads * 128 or \
+                not t.is_contiguous():
+            raise ValueError("k and v must be contiguous bf16 [seqs, tokens, heads*128]")
+    if k.shape != v.shape:
+        raise ValueError("k and v differ in shape")
+    _ok(load().rbd_kv8_read(ctypes.byref(c), _i32(lens, (c.seqs,), "lens"), k.shape[1], _ptr(k), c.heads * 128, _ptr(v),
+                            c.heads * 128, _stream(stream)), "rbd_kv8_read")
+
+
+def rbd_kv8_attn_workspace_bytes(seqs: int, heads: int, q_heads: int, rows: int, max_len: int,
+                                 weigh: bool = False) -> int:
+    """Bytes of device scratch rbd_kv8_attn needs (-1 for bad sizes)."""
+    return int(load().rbd_kv8_attn_workspace_bytes(seqs, heads, q_heads, rows, max_len, int(weigh)))
+
+
+def rbd_kv8_attn(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, codes: torch.Tensor,
+                 scales: torch.Tensor, o: torch.Tensor, q_heads: int, work: Optional[torch.Tensor], max_len: int,
+                 causal: bool = True, softmax_scale: float = 128 ** -0.5, weights_in: Optional[torch.Tensor] = None,
+                 weights_out: Optional[torch.Tensor] = None, code_format: int = CODES_INT8, stream=None) -> None:
+    """q bf16 [rows, >= q_heads*128] -> o bf16, attention over the cached tokens; weights_in / weights_out
+    float32 [seqs, heads, >= max_len] add up every key's attention weight (both or neither; the same one works)."""
+    c = _kv8(table, codes, scales, code_format)
+    ldq, ldo = _bf16_rows(q, q_heads * 128, "q"), _bf16_rows(o, q_heads * 128, "o")
+    if q.shape[0] != o.shape[0]:
+        raise ValueError("q and o differ in rows")
+    w_seq = w_head = 0
+    if (weights_in is None) != (weights_out is None):
+        raise ValueError("weights_in and weights_out go together")
+    if weights_out is not None:
+        w_seq, w_head, width = _weights(weights_out, c.seqs, c.heads, "weights_out")
+        if _weights(weights_in, c.seqs, c.heads, "weights_in") != (w_seq, w_head, width) or width < max_len:
+            raise ValueError("weights_in and weights_out must agree in shape and strides and hold max_len columns")
+    _ok(load().rbd_kv8_attn(ctypes.byref(c), _i32(lens, (c.seqs,), "lens"), _i32(cu, (c.seqs + 1,), "cu"), _ptr(q), ldq,
+                            q.shape[0], q_heads, int(causal), softmax_scale, max_len, _ptr(o), ldo, _ptr(weights_in),
+                            _ptr(weights_out), w_seq, w_head, _ptr(work),
+                            0 if work is None else work.numel() * work.element_size(), _stream(stream)),
+        "rbd_kv8_attn")
+
+
+def rbd_kv8_evict(weights: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, codes: torch.Tensor,
+                  scales: torch.Tensor, keep: int, recent: int, dst_table: torch.Tensor, kept: torch.Tensor,
+                  weights_out: torch.Tensor, lens_out: torch.Tensor, code_format: int = CODES_INT8,
+                  stream=None) -> None:
+    """Keep min(lens, keep) tokens of every (sequence, head): the last `recent` ones and those of largest weight
+    (weights float32 [seqs, heads, width >= lens]), quantised into the pages of dst_table int32 [seqs, >= ceil(keep / 64)]
+    (none of them held by a sequence).  kept int32 [seqs, heads, keep] gets the positions (-1 behind them),
+    weights_out float32 [seqs, heads, >= keep] their weights (zeros behind; may be weights), lens_out the new lengths."""
+    c = _kv8(table, codes, scales, code_format)
+    w_seq, w_head, width = _weights(weights, c.seqs, c.heads, "weights")
+    o_seq, o_head, width_out = _weights(weights_out, c.seqs, c.heads, "weights_out")
+    if dst_table.dtype != torch.int32 or dst_table.dim() != 2 or dst_table.shape[0] != c.seqs or \
+            dst_table.shape[1] * 64 < keep or (dst_table.shape[1] > 1 and dst_table.stride(1) != 1):
+        raise ValueError("dst_table must be row-major int32 [seqs, >= ceil(keep / 64)]")
+    ld_dst = dst_table.stride(0) if c.seqs > 1 else dst_table.shape[1]
+    _ok(load().rbd_kv8_evict(ctypes.byref(c), _i32(lens, (c.seqs,), "lens"), _ptr(weights), w_seq, w_head, width, keep,
+                             recent, _ptr(dst_table), ld_dst, _i32(kept, (c.seqs, c.heads, keep), "kept"),
+                             _ptr(weights_out), o_seq, o_head, width_out, _i32(lens_out, (c.seqs,), "lens_out"),
+                             _stream(stream)), "rbd_kv8_evict")
 
 
 def rbd_svdquant_fit(w: torch.Tensor, rank: int, omegas, bits: int = 4, rot_group: int = 256, scale_group: int = 0,

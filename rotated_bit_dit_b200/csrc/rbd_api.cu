@@ -12,6 +12,7 @@
 #include "rbd_common.cuh"
 
 #include "rbd_internal.cuh"
+#include "rbd_kv8.cuh"
 #include "rbd_rope.cuh"
 
 namespace {
@@ -605,6 +606,138 @@ rbd_status rbd_nvfp4_linear(const uint8_t* xq, const uint8_t* xbs, const float* 
   return cuda_status(rbd::launch_nvfp4_gemm(tm_x, tm_w, tm_ld, tm_l2, a, sms, as_stream(stream)));
 }
 
+namespace {
+rbd_status kv8_view(const rbd_kv8* c, rbd::Kv8View* out, bool* e4m3) {
+  if (!c) return RBD_ERR_INVALID_ARG;
+  if (c->code_format != RBD_CODES_INT8 && c->code_format != RBD_CODES_E4M3) return RBD_ERR_INVALID_ARG;
+  if (c->pages <= 0 || c->heads <= 0 || c->seqs < 0 || c->max_pages <= 0 || c->ldt < c->max_pages)
+    return RBD_ERR_INVALID_ARG;
+  // 32-bit token positions and grid dimensions
+  if (c->heads > 1024 || c->seqs > 65535 || c->pages > INT32_MAX || c->max_pages > (INT32_MAX >> 7))
+    return RBD_ERR_UNSUPPORTED;
+  if (!c->codes || !c->scales || (c->seqs > 0 && !c->table)) return RBD_ERR_INVALID_ARG;
+  if (!aligned16(c->codes) || (reinterpret_cast<uintptr_t>(c->scales) & 7u) ||
+      (reinterpret_cast<uintptr_t>(c->table) & 3u))
+    return RBD_ERR_ALIGNMENT;
+  *out = rbd::Kv8View{c->codes,
+                      c->scales,
+                      c->table,
+                      c->ldt,
+                      static_cast<int>(c->pages),
+                      c->heads,
+                      static_cast<int>(c->max_pages),
+                      static_cast<int>(c->seqs)};
+  *e4m3 = c->code_format == RBD_CODES_E4M3;
+  return RBD_OK;
+}
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+}  // namespace
+
+rbd_status rbd_kv8_append(const rbd_kv8* cache, const int32_t* lens, const int32_t* cu, const void* k, int64_t ldk,
+                          const void* v, int64_t ldv, int64_t rows, void* stream) {
+  rbd::Kv8View c;
+  bool e4m3;
+  const rbd_status s = kv8_view(cache, &c, &e4m3);
+  if (s != RBD_OK) return s;
+  if (rows < 0) return RBD_ERR_INVALID_ARG;
+  if (rows > (1 << 28)) return RBD_ERR_UNSUPPORTED;
+  if (rows == 0 || c.seqs == 0) return RBD_OK;
+  if (!lens || !cu || !k || !v || ldk < (int64_t)c.heads * 128 || ldv < (int64_t)c.heads * 128)
+    return RBD_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || (ldk % 8) || (ldv % 8) || !aligned4(lens) || !aligned4(cu))
+    return RBD_ERR_ALIGNMENT;
+  return cuda_status(rbd::launch_kv8_append(c, e4m3, lens, cu, static_cast<const uint16_t*>(k), ldk,
+                                            static_cast<const uint16_t*>(v), ldv, static_cast<int>(rows),
+                                            as_stream(stream)));
+}
+
+rbd_status rbd_kv8_read(const rbd_kv8* cache, const int32_t* lens, int64_t tokens, void* k, int64_t ldk, void* v,
+                        int64_t ldv, void* stream) {
+  rbd::Kv8View c;
+  bool e4m3;
+  const rbd_status s = kv8_view(cache, &c, &e4m3);
+  if (s != RBD_OK) return s;
+  if (tokens < 0) return RBD_ERR_INVALID_ARG;
+  if (tokens > INT32_MAX / 2 || (tokens > 0 && (int64_t)c.seqs * c.heads > (((int64_t)1 << 37) / tokens)))
+    return RBD_ERR_UNSUPPORTED;
+  if (tokens == 0 || c.seqs == 0) return RBD_OK;
+  if (!lens || !k || !v || ldk < (int64_t)c.heads * 128 || ldv < (int64_t)c.heads * 128) return RBD_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || (ldk % 8) || (ldv % 8) || !aligned4(lens)) return RBD_ERR_ALIGNMENT;
+  return cuda_status(rbd::launch_kv8_read(c, e4m3, lens, static_cast<int>(tokens), static_cast<uint16_t*>(k), ldk,
+                                          static_cast<uint16_t*>(v), ldv, as_stream(stream)));
+}
+
+namespace {
+rbd_status kv8_attn_sizes_ok(int64_t seqs, int64_t heads, int64_t q_heads, int64_t rows, int64_t max_len) {
+  if (seqs < 0 || heads <= 0 || q_heads <= 0 || rows < 0 || max_len < 0 || q_heads % heads != 0)
+    return RBD_ERR_INVALID_ARG;
+  if (seqs > 65535 || heads > 1024 || q_heads > 65536 || max_len > (1 << 30) || rows > ((int64_t)1 << 30) / q_heads)
+    return RBD_ERR_UNSUPPORTED;
+  return RBD_OK;
+}
+}  // namespace
+
+int64_t rbd_kv8_attn_workspace_bytes(int64_t seqs, int64_t heads, int64_t q_heads, int64_t rows, int64_t max_len,
+                                     int32_t weigh) {
+  if (kv8_attn_sizes_ok(seqs, heads, q_heads, rows, max_len) != RBD_OK) return -1;
+  if (seqs == 0) return 0;
+  return rbd::kv8_attn_workspace_bytes(static_cast<int>(seqs), static_cast<int>(heads), static_cast<int>(q_heads),
+                                       static_cast<int>(rows), static_cast<int>(max_len), weigh != 0);
+}
+
+rbd_status rbd_kv8_attn(const rbd_kv8* cache, const int32_t* lens, const int32_t* cu, const void* q, int64_t ldq,
+                        int64_t rows, int64_t q_heads, int32_t causal, float softmax_scale, int64_t max_len, void* o,
+                        int64_t ldo, const float* weights_in, float* weights_out, int64_t w_seq, int64_t w_head,
+                        void* work, int64_t work_bytes, void* stream) {
+  rbd::Kv8View c;
+  bool e4m3;
+  rbd_status s = kv8_view(cache, &c, &e4m3);
+  if (s != RBD_OK) return s;
+  s = kv8_attn_sizes_ok(c.seqs, c.heads, q_heads, rows, max_len);
+  if (s != RBD_OK) return s;
+  if (!(softmax_scale > 0.f) || !(softmax_scale < INFINITY)) return RBD_ERR_INVALID_ARG;
+  if (max_len > (int64_t)c.max_pages * 64 || (weights_in == nullptr) != (weights_out == nullptr))
+    return RBD_ERR_INVALID_ARG;
+  const bool weigh = weights_out != nullptr;
+  if (weigh && (w_head < max_len || w_seq < 0)) return RBD_ERR_INVALID_ARG;
+  if (c.seqs == 0 || (rows == 0 && !weigh)) return RBD_OK;
+  if (!lens || !cu || (rows > 0 && (!q || !o || ldq < q_heads * 128 || ldo < q_heads * 128))) return RBD_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || (ldq % 8) || (ldo % 8) || !aligned4(lens) || !aligned4(cu) ||
+      !aligned4(weights_in) || !aligned4(weights_out) || (reinterpret_cast<uintptr_t>(work) & 255u))
+    return RBD_ERR_ALIGNMENT;
+  const int64_t need = rbd_kv8_attn_workspace_bytes(c.seqs, c.heads, q_heads, rows, max_len, weigh);
+  if (need > 0 && (!work || work_bytes < need)) return RBD_ERR_INVALID_ARG;
+  return cuda_status(rbd::launch_kv8_attn(c, e4m3, lens, cu, static_cast<const uint16_t*>(q), ldq,
+                                          static_cast<int>(rows), static_cast<int>(q_heads), causal != 0,
+                                          softmax_scale * 1.4426950408889634f, static_cast<int>(max_len),
+                                          static_cast<uint16_t*>(o), ldo, weights_in, weights_out, w_seq, w_head, work,
+                                          as_stream(stream)));
+}
+
+rbd_status rbd_kv8_evict(const rbd_kv8* cache, const int32_t* lens, const float* weights, int64_t w_seq,
+                         int64_t w_head, int64_t width, int64_t keep, int64_t recent, const int32_t* dst_table,
+                         int64_t ld_dst, int32_t* kept, float* weights_out, int64_t o_seq, int64_t o_head,
+                         int64_t width_out, int32_t* lens_out, void* stream) {
+  rbd::Kv8View c;
+  bool e4m3;
+  const rbd_status s = kv8_view(cache, &c, &e4m3);
+  if (s != RBD_OK) return s;
+  if (keep <= 0 || recent < 0 || recent > keep || width <= 0 || width_out < keep || w_seq < 0 || o_seq < 0)
+    return RBD_ERR_INVALID_ARG;
+  if (width > (1 << 30) || width_out > (1 << 30) || keep > (int64_t)c.max_pages * 64) return RBD_ERR_UNSUPPORTED;
+  if (w_head < width || o_head < width_out || ld_dst < (keep + 63) / 64) return RBD_ERR_INVALID_ARG;
+  if (c.seqs == 0) return RBD_OK;
+  if (!lens || !weights || !dst_table || !kept || !weights_out || !lens_out) return RBD_ERR_INVALID_ARG;
+  if (lens_out == lens) return RBD_ERR_INVALID_ARG;     // read by blocks that may run after it is written
+  if (!aligned4(lens) || !aligned4(weights) || !aligned4(dst_table) || !aligned4(kept) || !aligned4(weights_out) ||
+      !aligned4(lens_out))
+    return RBD_ERR_ALIGNMENT;
+  return cuda_status(rbd::launch_kv8_evict(c, e4m3, weights, w_seq, w_head, static_cast<int>(width), weights_out,
+                                           o_seq, o_head, static_cast<int>(width_out), lens, lens_out, kept,
+                                           static_cast<int>(keep), static_cast<int>(recent), dst_table, ld_dst,
+                                           as_stream(stream)));
+}
+
 rbd_status rbd_check(void* stream) {
   cudaError_t e = cudaStreamSynchronize(as_stream(stream));
   if (e != cudaSuccess) return RBD_ERR_CUDA;
@@ -614,6 +747,12 @@ rbd_status rbd_check(void* stream) {
   if (st != 0) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(rbd::g_device_status, &zero, sizeof(int)) != cudaSuccess) return RBD_ERR_CUDA;
+    return static_cast<rbd_status>(st);
+  }
+  if (cudaMemcpyFromSymbol(&st, rbd::g_device_refusal, sizeof(int)) != cudaSuccess) return RBD_ERR_CUDA;
+  if (st != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(rbd::g_device_refusal, &zero, sizeof(int)) != cudaSuccess) return RBD_ERR_CUDA;
     return static_cast<rbd_status>(st);
   }
   return RBD_OK;

@@ -99,6 +99,23 @@ cudaError_t launch_attn_int8(const CUtensorMap& tm_q, const CUtensorMap& tm_k, c
                              const CUtensorMap& tm_sk, const float* sq, int Tq, int Tk, int H, uint16_t* o,
                              int64_t ldo, cudaStream_t st);
 
+// 8-bit paged key/value cache (Kv8View: rbd_kv8.cuh; e4m3: the codes' format).
+struct Kv8View;
+cudaError_t launch_kv8_append(const Kv8View& c, bool e4m3, const int32_t* lens, const int32_t* cu, const uint16_t* k,
+                              int64_t ldk, const uint16_t* v, int64_t ldv, int rows, cudaStream_t st);
+cudaError_t launch_kv8_read(const Kv8View& c, bool e4m3, const int32_t* lens, int tokens, uint16_t* k, int64_t ldk,
+                            uint16_t* v, int64_t ldv, cudaStream_t st);
+cudaError_t launch_kv8_evict(const Kv8View& c, bool e4m3, const float* weights, int64_t w_seq, int64_t w_head,
+                             int width, float* weights_out, int64_t o_seq, int64_t o_head, int width_out,
+                             const int32_t* lens, int32_t* lens_out, int32_t* kept, int keep, int recent,
+                             const int32_t* dst_table, int64_t ld_dst, cudaStream_t st);
+int64_t kv8_attn_workspace_bytes(int seqs, int heads, int q_heads, int rows, int max_len, bool weigh);
+// w_out null: no weights are summed.
+cudaError_t launch_kv8_attn(const Kv8View& c, bool e4m3, const int32_t* lens, const int32_t* cu, const uint16_t* q,
+                            int64_t ldq, int rows, int q_heads, bool causal, float scale_log2, int max_len,
+                            uint16_t* o, int64_t ldo, const float* w_in, float* w_out, int64_t w_seq, int64_t w_head,
+                            void* work, cudaStream_t st);
+
 // Offline SVDQuant fit (synchronous; host linear algebra between device steps).
 int64_t svdquant_workspace_bytes(int64_t n, int64_t k, int rank, int oversample, int bits, int scale_group);
 cudaError_t svdquant_fit(const uint16_t* w, int64_t n, int64_t k, int bits, bool rot, int scale_group, int rank,

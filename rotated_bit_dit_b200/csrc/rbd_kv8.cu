@@ -1,0 +1,411 @@
+// 8-bit paged key/value cache: append (quantise), read, and eviction by
+// accumulated attention weight.  The attention over it is in rbd_kv8_attn.cu.
+//
+// Quantisation of a page, per head and side, over its 64 x 128 values:
+//   s = max(s_old, RN(amax / qmax), 2^-100),  inv = RN(1 / s),
+//   code = round(RN(x * inv))  (to the nearest whole number in [-127, 127], or E4M3 value, ties to even)
+// with qmax = 127 (INT8) or 448 (E4M3), amax over the finite values that join
+// the page, and s_old the page's scale while it already holds tokens.  When the
+// scale grows, the older codes are formed again from the values they stand for,
+// which adds at most half a step of the new scale; among 64 tokens drawn alike a
+// running maximum moves H(64) = 4.7 times on average, so a page filled token by
+// token is requantised a handful of times, mostly while it is nearly empty.
+// The floor 2^-100 keeps 1 / s and the logarithms the attention takes finite; an
+// all-zero page then still lets later tokens set its scale.
+#include <algorithm>
+
+#include "rbd_kv8.cuh"
+#include "rbd_internal.cuh"
+
+namespace rbd {
+
+namespace {
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// Largest finite |bf16| bit pattern of a word's two values, max'ed into m (an infinity or NaN counts as zero).
+__device__ __forceinline__ uint32_t finite_amax(uint32_t m, uint32_t w) {
+  const uint32_t a = w & 0x7FFFu, b = (w >> 16) & 0x7FFFu;
+  return max(m, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t encode_bf16x4(uint32_t w0, uint32_t w1, float inv) {
+  return kv8_encode1<FMT>(bf16_lo(w0), inv) | (kv8_encode1<FMT>(bf16_hi(w0), inv) << 8) |
+         (kv8_encode1<FMT>(bf16_lo(w1), inv) << 16) | (kv8_encode1<FMT>(bf16_hi(w1), inv) << 24);
+}
+
+// Code of a stored code under a new scale: the value it stands for, quantised again.
+template <int FMT>
+__device__ __forceinline__ uint32_t requantise4(uint32_t w, float s_old, float inv) {
+  uint32_t o = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o |= kv8_encode1<FMT>(__fmul_rn(kv8_decode1<FMT>(w, j), s_old), inv) << (8 * j);
+  return o;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+}  // namespace
+
+// One block per (touched page, head): threads 0-127 the keys, 128-255 the values.
+// Thread l of a side takes 8 channels (16 bytes of bf16) of rows l / 16, l / 16 +
+// 8, ...: the page's new values stay in registers between the maximum and the
+// codes, so they are read once.  Bound by memory: 2 bytes in, 1 byte out a value.
+template <int FMT>
+__global__ void __launch_bounds__(256)
+    kv8_append_kernel(const Kv8View c, const int32_t* __restrict__ lens, const int32_t* __restrict__ cu,
+                      const uint16_t* __restrict__ k, int64_t ldk, const uint16_t* __restrict__ v, int64_t ldv,
+                      int rows) {
+  __shared__ uint32_t red[2][4];
+  auto pages_of = [&](int b) {
+    int r0, n;
+    if (!kv8_rows(cu, b, rows, r0, n) || n == 0) return 0;
+    const int len = __ldg(lens + b);
+    if (len < 0 || (int64_t)len + n > (int64_t)c.max_pages * kKv8Page) {
+      record_refusal();
+      return 0;
+    }
+    return (len + n - 1) / kKv8Page - len / kKv8Page + 1;
+  };
+  int b, idx;
+  if (!kv8_find(c.seqs, blockIdx.x, pages_of, b, idx)) return;
+  const int head = blockIdx.y;
+  const int len = __ldg(lens + b);
+  const int r0 = __ldg(cu + b), n = __ldg(cu + b + 1) - r0;
+  const int p = len / kKv8Page + idx;
+  const int page = kv8_page(c, b, p);
+  if (page < 0) return;
+  const int held = max(0, len - p * kKv8Page);                       // rows that already hold tokens
+  const int end = min(kKv8Page, len + n - p * kKv8Page);             // rows held afterwards
+  const int side = threadIdx.x >> 7, tid = threadIdx.x & 127;
+  const uint16_t* src = side ? v : k;
+  const int64_t ld = side ? ldv : ldk;
+  const int chunk8 = tid & 15, row0 = tid >> 4;
+  const int64_t first = (int64_t)r0 + (int64_t)p * kKv8Page - len;   // packed row of the page's row 0
+
+  uint4 raw[8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int t = row0 + 8 * i;
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (t >= held && t < end)
+      raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (first + t) * ld + head * kKv8Dim + 8 * chunk8));
+    m = finite_amax(finite_amax(finite_amax(finite_amax(m, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
+  }
+  float* scale = c.scales + kv8_scale(c, page, head, side);
+  const float s_old = held > 0 ? *scale : kKv8Floor;
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((tid & 31) == 0) red[side][tid >> 5] = m;
+  __syncthreads();
+  m = max(max(red[side][0], red[side][1]), max(red[side][2], red[side][3]));
+  const float amax = __uint_as_float(m << 16);
+  const float s = fmaxf(fmaxf(s_old, __fdiv_rn(amax, kv8_qmax<FMT>())), kKv8Floor);
+  const float inv = __frcp_rn(s);
+  uint8_t* tile = c.codes + kv8_tile(c, page, head, side);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int t = row0 + 8 * i;
+    uint2* dst = reinterpret_cast<uint2*>(tile + kv8_chunk(t, chunk8 >> 1) + 8 * (chunk8 & 1));
+    if (t >= held && t < end) {
+      *dst = make_uint2(encode_bf16x4<FMT>(raw[i].x, raw[i].y, inv), encode_bf16x4<FMT>(raw[i].z, raw[i].w, inv));
+    } else if (t < held && s > s_old) {
+      const uint2 w = *dst;
+      *dst = make_uint2(requantise4<FMT>(w.x, s_old, inv), requantise4<FMT>(w.y, s_old, inv));
+    }
+  }
+  if (tid == 0) *scale = s;
+}
+
+// The last `tokens` tokens of every sequence as bf16 rows [seqs * tokens]: a thread
+// per (row, head, 16-channel chunk), both sides.  Bound by memory: 1 byte in, 2 out.
+template <int FMT>
+__global__ void __launch_bounds__(256)
+    kv8_read_kernel(const Kv8View c, const int32_t* __restrict__ lens, int tokens, int64_t units,
+                    uint16_t* __restrict__ k, int64_t ldk, uint16_t* __restrict__ v, int64_t ldv) {
+  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (u >= units) return;
+  const int chunk = (int)(u & 7);
+  const int64_t rh = u >> 3;
+  const int64_t row = rh / c.heads;
+  const int head = (int)(rh - row * c.heads);
+  const int b = (int)(row / tokens);
+  const int i = (int)(row - (int64_t)b * tokens);
+  const int len = __ldg(lens + b);
+  const int64_t t = (int64_t)len - tokens + i;
+  int page = -1;
+  if (len < 0 || len > c.max_pages * kKv8Page) record_refusal();
+  else if (t >= 0) page = kv8_page(c, b, (int)(t / kKv8Page));
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    float s = 0.f;
+    if (page >= 0) {
+      w = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, page, head, side) +
+                                          kv8_chunk((int)(t % kKv8Page), chunk));
+      s = c.scales[kv8_scale(c, page, head, side)];
+    }
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      o[j] = pack_bf16(__fmul_rn(kv8_decode1<FMT>(ws[j >> 1], 2 * (j & 1)), s),
+                       __fmul_rn(kv8_decode1<FMT>(ws[j >> 1], 2 * (j & 1) + 1), s));
+    uint4* dst = reinterpret_cast<uint4*>((side ? v + row * ldv : k + row * ldk) + head * kKv8Dim + 16 * chunk);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Eviction
+// ---------------------------------------------------------------------------
+// Selection, one block of 1024 threads per (sequence, head): the last `recent`
+// tokens stay, and of the others the `keep - recent` of largest weight, equal
+// weights by the lowest position.  The weights become unsigned keys of the same
+// order, held in shared memory as far as they fit; three histogram passes (11, 11
+// and 10 bits from the top) find the key of the last one to stay and how many of
+// its equals stay with it; then every warp counts and emits its own run of
+// positions, so the kept ones come out in ascending order with no atomics on the
+// output and no dependence on timing.
+constexpr int kSelThreads = 1024;
+constexpr int kSelBins = 2048;
+constexpr int kSelMaxKeys = 48 * 1024;    // 192 KB of keys; positions beyond are read from global memory
+
+struct Kv8EvictArgs {
+  const float* weights;                    // [seqs][heads][width]
+  int64_t w_seq, w_head;
+  int width;
+  float* weights_out;                      // [seqs][heads][width_out], may be `weights`
+  int64_t o_seq, o_head;
+  int width_out;
+  const int32_t* lens;
+  int32_t* lens_out;
+  int32_t* kept;                           // [seqs][heads][keep]
+  int keep, recent;
+};
+
+__device__ __forceinline__ uint32_t order_key(float w) {
+  if (w != w) return 0u;                                    // a NaN is the first to go
+  const uint32_t u = __float_as_uint(w + 0.0f);             // -0 as +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8View c, const Kv8EvictArgs a, int cap) {
+  extern __shared__ uint32_t dyn[];
+  uint32_t* hist = dyn;                     // [kSelBins]
+  uint32_t* keys = dyn + kSelBins;          // [cap]
+  __shared__ uint32_t warp_sum[32], warp_eq[32];
+  __shared__ uint32_t sh_bin, sh_above;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.y, head = blockIdx.x;
+  int n = __ldg(a.lens + b);
+  if (n < 0 || n > a.width || n > c.max_pages * kKv8Page) {
+    if (tid == 0) record_refusal();
+    n = 0;
+  }
+  const float* w = a.weights + b * a.w_seq + head * a.w_head;
+  int32_t* kept = a.kept + ((int64_t)b * c.heads + head) * a.keep;
+  const int m = min(n, a.keep);
+  if (n <= a.keep) {
+    for (int j = tid; j < a.keep; j += kSelThreads) kept[j] = j < n ? j : -1;
+  } else {
+    const int cand = n - a.recent;          // positions that compete
+    int want = a.keep - a.recent;           // how many of them stay
+    for (int j = tid; j < a.recent; j += kSelThreads) kept[want + j] = cand + j;
+    for (int i = tid; i < cand && i < cap; i += kSelThreads) keys[i] = order_key(__ldg(w + i));
+    auto key = [&](int i) { return i < cap ? keys[i] : order_key(__ldg(w + i)); };
+    uint32_t prefix = 0, mask = 0;
+    uint32_t eq_want = (uint32_t)want;      // of the keys under the prefix, how many stay
+    if (want > 0) {
+      const int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
+#pragma unroll
+      for (int pass = 0; pass < 3; ++pass) {
+        for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+        __syncthreads();
+        const uint32_t bin_mask = (1u << bits[pass]) - 1u;
+        for (int i = tid; i < cand; i += kSelThreads) {
+          const uint32_t u = key(i);
+          if ((u & mask) == prefix) atomicAdd(&hist[(u >> shifts[pass]) & bin_mask], 1u);
+        }
+        __syncthreads();
+        // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
+        const uint32_t h0 = hist[kSelBins - 1 - 2 * tid], h1 = hist[kSelBins - 2 - 2 * tid];
+        uint32_t incl = h0 + h1;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const uint32_t up = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += up;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        uint32_t before = 0;
+        for (int i = 0; i < warp; ++i) before += warp_sum[i];
+        const uint32_t excl = before + incl - (h0 + h1);
+        if (excl < eq_want && eq_want <= excl + h0 + h1) {
+          const bool second = eq_want > excl + h0;
+          sh_bin = (uint32_t)(kSelBins - 1 - 2 * tid - (second ? 1 : 0));
+          sh_above = excl + (second ? h0 : 0u);
+        }
+        __syncthreads();
+        prefix |= sh_bin << shifts[pass];
+        mask |= bin_mask << shifts[pass];
+        eq_want -= sh_above;
+        __syncthreads();
+      }
+      // every warp takes a run of positions (a multiple of 32): counts, then the positions themselves
+      const int run = ((cand + 31) / 32 + 31) / 32 * 32;
+      const int i0 = warp * run, i1 = min(cand, i0 + run);
+      uint32_t gt = 0, eq = 0;
+      for (int i = i0; i < i1; i += 32) {
+        const uint32_t u = i + lane < i1 ? key(i + lane) : 0u;
+        gt += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && u > prefix));
+        eq += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && u == prefix));
+      }
+      if (lane == 0) {
+        warp_sum[warp] = gt;
+        warp_eq[warp] = eq;
+      }
+      __syncthreads();
+      uint32_t at_gt = 0, at_eq = 0;
+      for (int i = 0; i < warp; ++i) {
+        at_gt += warp_sum[i];
+        at_eq += warp_eq[i];
+      }
+      const uint32_t below = (1u << lane) - 1u;
+      for (int i = i0; i < i1; i += 32) {
+        const uint32_t u = i + lane < i1 ? key(i + lane) : 0u;
+        const uint32_t bg = __ballot_sync(0xffffffffu, i + lane < i1 && u > prefix);
+        const uint32_t be = __ballot_sync(0xffffffffu, i + lane < i1 && u == prefix);
+        const uint32_t my_eq = at_eq + __popc(be & below);       // equals in front of this position
+        const uint32_t pos = at_gt + __popc(bg & below) + min(my_eq, eq_want);
+        if (i + lane < i1 && (u > prefix || (u == prefix && my_eq < eq_want))) kept[pos] = i + lane;
+        at_gt += __popc(bg);
+        at_eq += __popc(be);
+      }
+    }
+  }
+  __syncthreads();
+  // weights of the kept tokens, ascending; safe in place, since position j never comes from below j and a
+  // chunk is read before it is written
+  float* wo = a.weights_out + b * a.o_seq + head * a.o_head;
+  for (int j0 = 0; j0 < m; j0 += kSelThreads) {
+    const int j = j0 + tid;
+    const float x = j < m ? w[kept[j]] : 0.f;
+    __syncthreads();
+    if (j < m) wo[j] = x;
+    __syncthreads();
+  }
+  for (int j = m + tid; j < a.width_out; j += kSelThreads) wo[j] = 0.f;
+  if (head == 0 && tid == 0) a.lens_out[b] = m;
+}
+
+// The kept tokens into fresh pages, one block per (page, head, sequence): threads
+// 0-127 the keys, 128-255 the values, 16 channels of 4 rows each, read once and
+// kept in registers between the maximum and the new codes.
+template <int FMT>
+__global__ void __launch_bounds__(256)
+    kv8_gather_kernel(const Kv8View c, const int32_t* __restrict__ dst_table, int64_t ld_dst,
+                      const int32_t* __restrict__ kept, const int32_t* __restrict__ lens_out, int keep) {
+  __shared__ uint32_t red[2][4];
+  const int b = blockIdx.z, head = blockIdx.y, p = blockIdx.x;
+  const int m = min(__ldg(lens_out + b), keep);
+  const int end = min(kKv8Page, m - p * kKv8Page);
+  if (end <= 0) return;
+  const int dst_page = __ldg(dst_table + b * ld_dst + p);
+  if (dst_page < 0 || dst_page >= c.pages) {
+    if (threadIdx.x == 0) record_refusal();
+    return;
+  }
+  const int side = threadIdx.x >> 7, tid = threadIdx.x & 127;
+  const int chunk = tid & 7, row0 = tid >> 3;
+  const int32_t* from = kept + ((int64_t)b * c.heads + head) * keep + p * kKv8Page;
+  uint4 raw[4];
+  float s_src[4];
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = row0 + 16 * i;
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    s_src[i] = 0.f;
+    if (t < end) {
+      const int src = __ldg(from + t);
+      const int page = kv8_page(c, b, src / kKv8Page);
+      if (page >= 0) {
+        raw[i] = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, page, head, side) +
+                                                 kv8_chunk(src % kKv8Page, chunk));
+        s_src[i] = c.scales[kv8_scale(c, page, head, side)];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t ws[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(kv8_decode1<FMT>(ws[j >> 2], j & 3)));
+    am = fmaxf(am, __fmul_rn(top, s_src[i]));
+  }
+  const uint32_t m_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
+  if ((tid & 31) == 0) red[side][tid >> 5] = m_bits;
+  __syncthreads();
+  am = __uint_as_float(max(max(red[side][0], red[side][1]), max(red[side][2], red[side][3])));
+  const float s = fmaxf(__fdiv_rn(am, kv8_qmax<FMT>()), kKv8Floor);
+  const float inv = __frcp_rn(s);
+  uint8_t* tile = c.codes + kv8_tile(c, dst_page, head, side);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = row0 + 16 * i;
+    if (t < end)
+      *reinterpret_cast<uint4*>(tile + kv8_chunk(t, chunk)) =
+          make_uint4(requantise4<FMT>(raw[i].x, s_src[i], inv), requantise4<FMT>(raw[i].y, s_src[i], inv),
+                     requantise4<FMT>(raw[i].z, s_src[i], inv), requantise4<FMT>(raw[i].w, s_src[i], inv));
+  }
+  if (tid == 0) c.scales[kv8_scale(c, dst_page, head, side)] = s;
+}
+
+// ---------------------------------------------------------------------------
+// Host launchers
+// ---------------------------------------------------------------------------
+cudaError_t launch_kv8_append(const Kv8View& c, bool e4m3, const int32_t* lens, const int32_t* cu, const uint16_t* k,
+                              int64_t ldk, const uint16_t* v, int64_t ldv, int rows, cudaStream_t st) {
+  // n tokens touch at most (n - 1) / 64 + 2 pages; never more than one page a token
+  const int64_t items = std::min<int64_t>(rows, (int64_t)rows / kKv8Page + 2 * (int64_t)std::min(c.seqs, rows));
+  const dim3 grid((unsigned)items, c.heads);
+  if (e4m3) kv8_append_kernel<RBD_CODES_E4M3><<<grid, 256, 0, st>>>(c, lens, cu, k, ldk, v, ldv, rows);
+  else kv8_append_kernel<RBD_CODES_INT8><<<grid, 256, 0, st>>>(c, lens, cu, k, ldk, v, ldv, rows);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv8_read(const Kv8View& c, bool e4m3, const int32_t* lens, int tokens, uint16_t* k, int64_t ldk,
+                            uint16_t* v, int64_t ldv, cudaStream_t st) {
+  const int64_t units = (int64_t)c.seqs * tokens * c.heads * 8;
+  const unsigned grid = (unsigned)((units + 255) / 256);
+  if (e4m3) kv8_read_kernel<RBD_CODES_E4M3><<<grid, 256, 0, st>>>(c, lens, tokens, units, k, ldk, v, ldv);
+  else kv8_read_kernel<RBD_CODES_INT8><<<grid, 256, 0, st>>>(c, lens, tokens, units, k, ldk, v, ldv);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv8_evict(const Kv8View& c, bool e4m3, const float* weights, int64_t w_seq, int64_t w_head,
+                             int width, float* weights_out, int64_t o_seq, int64_t o_head, int width_out,
+                             const int32_t* lens, int32_t* lens_out, int32_t* kept, int keep, int recent,
+                             const int32_t* dst_table, int64_t ld_dst, cudaStream_t st) {
+  const Kv8EvictArgs a{weights, w_seq, w_head, width, weights_out, o_seq, o_head, width_out,
+                       lens,    lens_out, kept, keep,  recent};
+  const int cap = std::min(std::min(width, c.max_pages * kKv8Page), kSelMaxKeys);
+  const int smem = (kSelBins + cap) * 4;
+  cudaError_t e = cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (kSelBins + kSelMaxKeys) * 4);
+  if (e != cudaSuccess) return e;
+  kv8_select_kernel<<<dim3(c.heads, c.seqs), kSelThreads, smem, st>>>(c, a, cap);
+  const dim3 grid((keep + kKv8Page - 1) / kKv8Page, c.heads, c.seqs);
+  if (e4m3) kv8_gather_kernel<RBD_CODES_E4M3><<<grid, 256, 0, st>>>(c, dst_table, ld_dst, kept, lens_out, keep);
+  else kv8_gather_kernel<RBD_CODES_INT8><<<grid, 256, 0, st>>>(c, dst_table, ld_dst, kept, lens_out, keep);
+  return cudaGetLastError();
+}
+
+}  // namespace rbd

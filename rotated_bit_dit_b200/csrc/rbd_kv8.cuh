@@ -1,0 +1,145 @@
+// Shared pieces of the 8-bit paged key/value cache: the view of a cache that
+// kernels receive, the layout of a page, the code conversions and the mapping
+// of a launch's items to sequences.
+//
+// A page holds 64 consecutive tokens of one sequence.  codes is
+// [pages][heads][2][64][128] bytes (side 0 keys, side 1 values): one (page,
+// head) is 16 KB of contiguous memory, one bulk copy.  Inside a [64][128] tile
+// the eight 16-byte chunks of token row t are permuted, chunk c standing at
+// c ^ (t & 7): the fragment reads of the single-token kernel (eight lanes, two
+// chunks of four token rows or the same chunk of four) then touch all 32 banks
+// once, with no copy between the bulk load and the registers.  scales is
+// [pages][heads][2] float32; value = code * scale.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "rbd_common.cuh"
+
+namespace rbd {
+
+// First refusal of device-side metadata (a page index outside the pool, offsets
+// or lengths outside their buffers) since the last rbd_check.  Kept apart from
+// g_device_status, which makes bounded waits give up.
+__device__ int g_device_refusal = 0;
+__device__ __forceinline__ void record_refusal() { atomicCAS(&g_device_refusal, 0, RBD_ERR_INVALID_ARG); }
+
+constexpr int kKv8Page = 64;                       // tokens per page
+constexpr int kKv8Dim = 128;                       // channels per head
+constexpr int kKv8Side = kKv8Page * kKv8Dim;       // bytes of one side of a (page, head)
+constexpr float kKv8Floor = 7.888609052210118e-31f;   // 2^-100: smallest scale
+
+struct Kv8View {
+  uint8_t* codes;
+  float* scales;
+  const int32_t* table;   // [seqs][ldt]
+  int64_t ldt;
+  int pages, heads, max_pages, seqs;
+};
+
+// Byte offset of (token t, channel chunk c of 16) inside a [64][128] tile.
+__host__ __device__ __forceinline__ constexpr int kv8_chunk(int t, int c) { return t * kKv8Dim + ((c ^ (t & 7)) << 4); }
+
+__device__ __forceinline__ int64_t kv8_tile(const Kv8View& c, int page, int head, int side) {
+  return ((((int64_t)page * c.heads + head) * 2) + side) * kKv8Side;
+}
+__device__ __forceinline__ int64_t kv8_scale(const Kv8View& c, int page, int head, int side) {
+  return ((int64_t)page * c.heads + head) * 2 + side;
+}
+
+// Page p of sequence b, or -1 (recorded) when the table names none of the pool.
+__device__ __forceinline__ int kv8_page(const Kv8View& c, int b, int p) {
+  const int page = __ldg(c.table + (int64_t)b * c.ldt + p);
+  if (page >= 0 && page < c.pages) return page;
+  record_refusal();
+  return -1;
+}
+
+// Rows [cu[b], cu[b+1]) of a packed tensor of `rows` rows; false (recorded) when they lie outside it.
+__device__ __forceinline__ bool kv8_rows(const int32_t* cu, int b, int rows, int& r0, int& n) {
+  const int a = __ldg(cu + b), z = __ldg(cu + b + 1);
+  r0 = a;
+  n = z - a;
+  if (a >= 0 && z >= a && z <= rows) return true;
+  record_refusal();
+  n = 0;
+  return false;
+}
+
+// Which sequence item x belongs to, when sequence b has count(b) items in a row:
+// b and the item's index inside it.  Every warp of the block finds out by itself
+// (32 sequences per step, an inclusive scan of their counts); all 32 lanes call.
+template <class Count>
+__device__ __forceinline__ bool kv8_find(int seqs, int x, Count count, int& b, int& idx) {
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+  for (int b0 = 0; b0 < seqs; b0 += 32) {
+    int c = b0 + lane < seqs ? count(b0 + lane) : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, c, off);
+      if (lane >= off) c += up;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, x < base + c);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      const int before = __shfl_sync(0xffffffffu, c, l > 0 ? l - 1 : 0);
+      b = b0 + l;
+      idx = x - base - (l > 0 ? before : 0);
+      return true;
+    }
+    base += __shfl_sync(0xffffffffu, c, 31);
+  }
+  return false;
+}
+
+template <int FMT>
+__host__ __device__ __forceinline__ constexpr float kv8_qmax() { return FMT == RBD_CODES_INT8 ? 127.f : 448.f; }
+
+// Code of x under the inverse scale inv; a NaN is stored as zero, an infinity as the largest code.
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_encode1(float x, float inv) {
+  const float y = __fmul_rn(x, inv);
+  if (FMT == RBD_CODES_INT8) {
+    int q = __float2int_rn(y);                      // saturates; NaN gives 0
+    q = q > 127 ? 127 : (q < -127 ? -127 : q);
+    return (uint32_t)q & 0xFFu;
+  }
+  return y != y ? 0u : (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Value of code byte j of word w (0 <= j < 4).
+template <int FMT>
+__device__ __forceinline__ float kv8_decode1(uint32_t w, int j) {
+  const uint32_t byte = (w >> (8 * j)) & 0xFFu;
+  if (FMT == RBD_CODES_INT8) return (float)(int8_t)byte;
+  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3);
+  return __half2float(__half(h));
+}
+
+// Four code bytes -> two fp16 pairs.  INT8: (b0, b2) and (b1, b3); the byte with its sign bit flipped, under the
+// exponent of 1024, is 1024 + 128 + b, from which one subtraction leaves b exactly.  E4M3: (b0, b1) and (b2, b3),
+// every E4M3 value being an fp16 value.
+__device__ __forceinline__ uint32_t hsub2_u(uint32_t a, uint32_t b) {
+  __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t m, uint32_t x) { return (a & m) ^ x; }
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(two));
+  return d;
+}
+template <int FMT>
+__device__ __forceinline__ void kv8_to_f16(uint32_t w, uint32_t& p0, uint32_t& p1) {
+  if (FMT == RBD_CODES_INT8) {
+    p0 = hsub2_u(and_xor(w, 0x00FF00FFu, 0x64806480u), 0x64806480u);
+    p1 = hsub2_u(and_xor(w >> 8, 0x00FF00FFu, 0x64806480u), 0x64806480u);
+  } else {
+    p0 = e4m3x2_to_f16x2(w & 0xFFFFu);
+    p1 = e4m3x2_to_f16x2(w >> 16);
+  }
+}
+
+}  // namespace rbd

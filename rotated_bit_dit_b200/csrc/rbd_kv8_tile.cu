@@ -1,0 +1,749 @@
+// Attention over the 8-bit paged cache for many query rows: the tensor-core
+// kernels.  The mathematics (value scales in the exponent, power-of-two query
+// scaling) is described in rbd_kv8_attn.cu.
+//
+// kv8_tile_kernel, one block per 256 rows (two query tiles of 128) of one
+// (sequence, key/value head) and one split of its keys; four warpgroups:
+//   0, 1   softmax of query tile 0 / 1, one row per thread (TMEM lane = row);
+//   2      converters: codes from global memory to fp16 operands in shared memory;
+//   3      one warp: TMEM owner and MMA issuer.
+// Per 128-key step (two pages) and query tile t: S_t = Q_t K^T into TMEM columns
+// 128 t .. (fp16 operands from shared memory), the softmax writes P_t as fp16 over
+// the first 64 of those columns, and O_t += P_t V takes P_t from TMEM and V from
+// shared memory as it is stored, token by token (an MN-major operand), so V is
+// never transposed.  The issuer interleaves the tiles: while softmax t works, the
+// tensor core runs P.V and Q.K^T of the other tile.
+// Converting inside the kernel keeps global traffic at one byte per value and puts
+// the work on warps that have issue slots to spare: a 128-key step is 32 KB of
+// codes for 16.8 MFLOP.
+#include "rbd_kv8.cuh"
+#include "rbd_internal.cuh"
+
+namespace rbd {
+
+namespace {
+
+constexpr int kTlRows = 128;                       // rows of a query tile (TMEM lanes)
+constexpr int kTlKeys = 128;                       // keys per step
+constexpr int kTlThreads = 512;
+constexpr uint32_t kTlTile = 32768;                // a 128 x 128 fp16 operand: two 64-channel halves of 128-byte rows
+constexpr uint32_t kTlK = 2 * kTlTile;             // keys, 2 stages
+constexpr uint32_t kTlV = kTlK + 2 * kTlTile;      // values, 2 stages
+constexpr uint32_t kTlScale = kTlV + 2 * kTlTile;  // page scales: 4 slots x 2 pages x (s_k, log2 s_v, 1 / s_v, -)
+constexpr uint32_t kTlCoef = kTlScale + 4 * 32;    // base-2 score factor of the 256 rows
+constexpr uint32_t kTlBar = kTlCoef + 256 * 4;
+constexpr uint32_t kTlSmem = kTlBar + 256 + 1024;  // + alignment slack
+
+// Shared-memory descriptor of an MN-major fp16 operand with the 128-byte swizzle: rows of 64 MN elements (128
+// bytes), one row per K index; 8-row groups sbo bytes apart along K, 64-element blocks lbo bytes apart along MN.
+__device__ __forceinline__ uint64_t smem_desc_mnmajor(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit float inputs, fp32 accumulation.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+constexpr uint32_t kIdescBMn = 1u << 16;           // B is MN-major
+
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Byte offset of 16-byte chunk ch (0..15, 8 channels each) of row t in a 128 x 128 fp16 operand.
+__device__ __forceinline__ uint32_t tile_chunk(int t, int ch) {
+  return (uint32_t)(ch >> 3) * 16384u + (uint32_t)t * 128u + (uint32_t)(((ch & 7) ^ (t & 7)) << 4);
+}
+
+// Sixteen codes of one token as fp16, channels 16 c .. 16 c + 15, into an operand tile.
+template <int FMT>
+__device__ __forceinline__ void store_codes(unsigned char* tile, int t, int c, const uint4& w) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    kv8_to_f16<FMT>(FMT == RBD_CODES_INT8 ? prmt(ws[i], 0u, 0x3120u) : ws[i], h[2 * i], h[2 * i + 1]);
+  *reinterpret_cast<uint4*>(tile + tile_chunk(t, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<uint4*>(tile + tile_chunk(t, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+}  // namespace
+
+template <int FMT>
+__global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c, const Kv8AttnArgs a) {
+  extern __shared__ unsigned char smem_dyn[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023u) & ~uintptr_t(1023u));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kTlBar);
+  uint64_t* k_full = bars;          // [2] 4 converter warps
+  uint64_t* k_empty = bars + 2;     // [2] commit
+  uint64_t* v_full = bars + 4;      // [2]
+  uint64_t* v_empty = bars + 6;     // [2]
+  uint64_t* s_full = bars + 8;      // [2] per query tile, commit
+  uint64_t* p_full = bars + 10;     // [2] per query tile, 4 softmax warps
+  uint64_t* sc_full = bars + 12;    // [4] the two page scales of a step
+  uint64_t* o_done = bars + 16;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 18);
+  float* coef = reinterpret_cast<float*>(smem + kTlCoef);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = blockIdx.y, split = blockIdx.z;
+  // items of a launch run from the last to the first: with a causal mask the later rows of a sequence see the
+  // most keys, and long blocks had better start early
+  const int item = a.items - 1 - (int)blockIdx.x;
+  auto tiles_of = [&](int b) {
+    int r0, n;
+    kv8_rows(a.cu, b, a.rows, r0, n);
+    return (int)(((int64_t)n * a.group + 2 * kTlRows - 1) / (2 * kTlRows));
+  };
+  int b, tile;
+  if (!kv8_find(c.seqs, item, tiles_of, b, tile)) return;
+  int r0, n;
+  kv8_rows(a.cu, b, a.rows, r0, n);
+  const int len = kv8_len(c, a, b);
+  const int row_first = tile * 2 * kTlRows;
+  const int nrows = min(2 * kTlRows, n * a.group - row_first);
+  // 128-key steps of either query tile, and the ones of this split
+  int steps[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(nrows, (t + 1) * kTlRows) - 1;
+    const int vis = last >= t * kTlRows ? min(len, kv8_visible(a.causal, len, n, (row_first + last) / a.group)) : 0;
+    steps[t] = (vis + kTlKeys - 1) / kTlKeys;
+  }
+  const int all = max(steps[0], steps[1]);
+  const int per = (all + a.nsplit - 1) / a.nsplit;
+  const int j0 = split * per, j1 = min(all, j0 + per);
+  const int cnt = max(0, j1 - j0);
+  int cnt_t[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) cnt_t[t] = max(0, min(j1, steps[t]) - j0);
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 4);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 4);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&sc_full[i], 2);
+    mbar_init(o_done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  // Queries: bf16 rows to fp16 tiles, 16 lanes a row
+  for (int r = warp * 2 + (lane >> 4); r < 2 * kTlRows; r += 32) {
+    const int ch = lane & 15;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (r < nrows) {
+      const int rr = row_first + r;
+      w = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(r0 + rr / a.group) * a.ldq +
+                                               (int64_t)(head * a.group + rr % a.group) * kKv8Dim + 8 * ch));
+    }
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    uint32_t amax = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) amax = max(amax, max(ws[e] & 0x7FFFu, (ws[e] >> 16) & 0x7FFFu));
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    float f, inv;
+    kv8_row_scale(amax, f, inv);
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      h[e] = half2_bits(__uint_as_float(ws[e] << 16) * f, __uint_as_float(ws[e] & 0xFFFF0000u) * f);
+    const uint4 hv = make_uint4(h[0], h[1], h[2], h[3]);
+    const int t = r >> 7, tr = r & 127;
+    *reinterpret_cast<uint4*>(smem + t * kTlTile + tile_chunk(tr, ch)) = hv;
+    if (ch == 0) coef[r] = inv * a.scale_log2;
+    if (a.q_image && split == 0) {
+      const int64_t img = ((int64_t)head * a.items + item) * 2 + t;
+      *reinterpret_cast<uint4*>(a.q_image + img * kTlTile + tile_chunk(tr, ch)) = hv;
+      if (ch == 0) a.q_coef[img * kTlRows + tr] = inv * a.scale_log2;
+    }
+  }
+  fence_async_shared();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp >= 12) {
+    // ------------------------------------------------------------ MMA issuer
+    reg_dec<40>();
+    if (warp == 12 && elect_one() && cnt > 0) {
+      const uint32_t id_qk = idesc_f16(kTlRows, kTlKeys);
+      const uint32_t id_pv = idesc_f16(kTlRows, kKv8Dim) | kIdescBMn;
+      bool ok = true;
+      auto issue_qk = [&](int t, int j) {
+        const uint32_t qb = smem_u32(smem + t * kTlTile), kb = smem_u32(smem + kTlK + (j & 1) * kTlTile);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
+          mma_bf16_ss(tmem + t * kTlKeys, smem_desc_kmajor(qb + off, 128), smem_desc_kmajor(kb + off, 128), id_qk,
+                      kk > 0);
+        }
+        tc_commit(&s_full[t]);
+      };
+      ok = mbar_wait(&k_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t)
+          if (cnt_t[t] > 0) issue_qk(t, 0);
+        tc_commit(&k_empty[0]);
+      }
+      for (int j = 0; j < cnt && ok; ++j) {
+        if (!mbar_wait(&v_full[j & 1], (j >> 1) & 1)) { ok = false; break; }
+        if (j + 1 < cnt && !mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) { ok = false; break; }
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (j >= cnt_t[t]) continue;
+          if (!mbar_wait(&p_full[t], j & 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t vb = smem_u32(smem + kTlV + (j & 1) * kTlTile);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_ts(tmem + 256 + t * kKv8Dim, tmem + t * kTlKeys + 8 * kk,
+                       smem_desc_mnmajor(vb + kk * 2048, 16384, 1024), id_pv, (j > 0 || kk > 0) ? 1u : 0u);
+          if (j + 1 < cnt_t[t]) issue_qk(t, j + 1);
+        }
+        if (!ok) break;
+        tc_commit(&v_empty[j & 1]);
+        if (j + 1 < cnt) tc_commit(&k_empty[(j + 1) & 1]);
+      }
+      tc_commit(o_done);
+      mbar_wait(o_done, 0, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ converters
+    // a warp takes 32 tokens of a step (half a page); a lane, 16 channels of 8 of them
+    reg_dec<104>();
+    const int w4 = warp - 8;
+    uint4 raw[2][8];
+    float2 sc = make_float2(1.f, 1.f);
+    auto fetch = [&](int side, int j) {
+      const int p = (j0 + j) * 2 + (w4 >> 1);
+      const int held = len - p * kKv8Page;                     // tokens of the page
+      const int page = held > 0 ? kv8_page(c, b, p) : -1;
+      const uint8_t* src = page >= 0 ? c.codes + kv8_tile(c, page, head, side) : nullptr;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = 32 * (w4 & 1) + 8 * (i >> 1) + (lane >> 2);
+        const int ch = (lane & 3) + 4 * (i & 1);
+        raw[side][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (src && row < held) raw[side][i] = *reinterpret_cast<const uint4*>(src + kv8_chunk(row, ch));
+      }
+      if (side == 0) {
+        sc = make_float2(1.f, 1.f);
+        if (page >= 0) sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page, head, 0));
+      }
+    };
+    auto put = [&](int side, int j) {
+      unsigned char* dst = smem + (side ? kTlV : kTlK) + (j & 1) * kTlTile;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        store_codes<FMT>(dst, 32 * w4 + 8 * (i >> 1) + (lane >> 2), (lane & 3) + 4 * (i & 1), raw[side][i]);
+    };
+    if (cnt > 0) {
+      fetch(0, 0);
+      fetch(1, 0);
+    }
+    for (int j = 0; j < cnt; ++j) {
+      const uint32_t par = ((j >> 1) & 1) ^ 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[j & 1], par))) break;
+      put(0, j);
+      // Slot j % 4 was last read for step j - 4, whose P V (awaited before its K stage came free for step j - 2)
+      // follows that softmax.
+      if ((w4 & 1) == 0 && lane == 0)
+        *reinterpret_cast<float4*>(smem + kTlScale + (j & 3) * 32 + (w4 >> 1) * 16) =
+            make_float4(sc.x, log2f(sc.y), 1.0f / sc.y, 0.f);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[j & 1]);
+      if ((w4 & 1) == 0 && lane == 0) mbar_arrive(&sc_full[j & 3]);
+      if (j + 1 < cnt) fetch(0, j + 1);
+      if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[j & 1], par))) break;
+      put(1, j);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[j & 1]);
+      if (j + 1 < cnt) fetch(1, j + 1);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    reg_inc<184>();
+    const int t = warp >> 2;
+    const int r = tid;                                          // row of the block
+    const bool live = r < nrows;
+    const int rr = row_first + r;
+    const int lim = live ? kv8_visible(a.causal, len, n, rr / a.group) : 0;
+    const int min_lim = __reduce_min_sync(0xffffffffu, live ? lim : 0x7FFFFFFF);
+    const float cq = coef[r];
+    const uint32_t lane_addr = (32u * (uint32_t)(warp & 3)) << 16;
+    const uint32_t t_s = tmem + lane_addr + t * kTlKeys, t_o = tmem + lane_addr + 256 + t * kKv8Dim;
+    auto wait_warp = [](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+    };
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    const int mine = cnt_t[t];
+    for (int j = 0; j < mine; ++j) {
+      if (!wait_warp(&sc_full[j & 3], (j >> 2) & 1) || !wait_warp(&s_full[t], j & 1)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, s + 32 * q);
+      const float4 sc0 = *reinterpret_cast<const float4*>(smem + kTlScale + (j & 3) * 32);
+      const float4 sc1 = *reinterpret_cast<const float4*>(smem + kTlScale + (j & 3) * 32 + 16);
+      tmem_wait_ld();
+#pragma unroll
+      for (int q = 0; q < 8; ++q) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(s + 16 * q));
+      const int k0 = (j0 + j) * kTlKeys;
+      const bool full = min_lim >= k0 + kTlKeys;                // the warp's rows all see every key of the step
+      const int nv = lim - k0;
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e >= nv) s[e] = 0xFF800000u;                      // -inf
+      }
+      float mx[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(s[(e >> 2) * 64 + (e & 3)]);
+#pragma unroll
+      for (int e = 4; e < 64; ++e) {
+        mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+        mx[4 + (e & 3)] = fmaxf(mx[4 + (e & 3)], __uint_as_float(s[64 + e]));
+      }
+      const float mx0 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const float mx1 = fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+      const float c0 = cq * sc0.x, c1 = cq * sc1.x;
+      const float mt = fmaxf(mx0 > -INFINITY ? fmaf(mx0, c0, sc0.y) : -INFINITY,
+                             mx1 > -INFINITY ? fmaf(mx1, c1, sc1.y) : -INFINITY);
+      const bool move = mt > m_run + kKv8Lazy;
+      if (__any_sync(0xffffffffu, move)) {
+        const float f = move ? ex2(m_run - mt) : 1.f;
+        if (j > 0) {       // O holds steps 0 .. j - 1: their P V precede S of step j on the tensor core
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t ov[32];
+            tmem_ld32(t_o + 32 * q, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+            tmem_st32(t_o + 32 * q, ov);
+          }
+          tmem_wait_st();
+        }
+        l_run *= f;
+        if (move) m_run = mt;
+      }
+      const float m_use = m_run > -INFINITY ? m_run : 0.f;
+      const float b0 = sc0.y - m_use, b1 = sc1.y - m_use;
+      float lp[4] = {0.f, 0.f, 0.f, 0.f};
+      // (a score factor of zero, from a vanishing query, would turn a masked -inf into a NaN: masked keys get p = 0)
+#pragma unroll
+      for (int e = 0; e < 128; e += 2) {
+        const float cc = e < 64 ? c0 : c1, bb = e < 64 ? b0 : b1;
+        float x = ex2(fmaf(__uint_as_float(s[e]), cc, bb)), y = ex2(fmaf(__uint_as_float(s[e + 1]), cc, bb));
+        if (!full) {
+          x = e < nv ? x : 0.f;
+          y = e + 1 < nv ? y : 0.f;
+        }
+        lp[(e >> 6) * 2] += x;
+        lp[(e >> 6) * 2 + 1] += y;
+        s[e >> 1] = half2_bits(x, y);
+      }
+      l_run = fmaf(lp[0] + lp[1], sc0.z, l_run);
+      l_run = fmaf(lp[2] + lp[3], sc1.z, l_run);
+      tmem_st32(t_s, s);
+      tmem_st32(t_s + 32, s + 32);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[t]);
+    }
+    // output: O / L, or the split's O, m and L
+    const bool have = mine > 0;
+    ok = ok && (cnt == 0 || wait_warp(o_done, 0));
+    tc_fence_after();
+    if (ok) {
+      const int qh = head * a.group + rr % a.group;
+      const int64_t tok = r0 + rr / a.group;
+      const int64_t fr = tok * a.q_heads + qh;
+      const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
+      const bool whole = a.nsplit == 1;
+      if (live && !whole) a.part_ml[fr * a.nsplit + split] = make_float2(m_run, l_run);
+      if (live && whole && a.stats) a.stats[fr] = make_float2(m_run > -INFINITY ? m_run : 0.f, inv);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t ov[32];
+        if (have) {
+          tmem_ld32(t_o + 32 * q, ov);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = 0u;
+        }
+        if (!live) continue;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.o + tok * a.ldo + (int64_t)qh * kKv8Dim + 32 * q);
+#pragma unroll
+          for (int e8 = 0; e8 < 4; ++e8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e2 = 0; e2 < 4; ++e2) {
+              const __nv_bfloat162 p2 = __floats2bfloat162_rn(__uint_as_float(ov[8 * e8 + 2 * e2]) * inv,
+                                                              __uint_as_float(ov[8 * e8 + 2 * e2 + 1]) * inv);
+              w[e2] = *reinterpret_cast<const uint32_t*>(&p2);
+            }
+            dst[e8] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (have) {
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + (fr * a.nsplit + split) * kKv8Dim + 32 * q);
+#pragma unroll
+          for (int e4 = 0; e4 < 8; ++e4) dst[e4] = make_uint4(ov[4 * e4], ov[4 * e4 + 1], ov[4 * e4 + 2], ov[4 * e4 + 3]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Weights of the keys, many query rows
+// ---------------------------------------------------------------------------
+// A block per (128 keys, key/value head, sequence) computes S^T = K Q^T for every
+// query tile that sees them, the keys on the TMEM lanes: a thread owns a key and
+// adds 2^(x - m) / L over the columns, with the rows' final m and L, in a fixed
+// order and without atomics.  The query tiles come from the images the attention
+// left behind (one 32 KB bulk copy each).
+//   warps 0-3, 4-7  sums, query tiles in turn;  warp 8  producer;  warp 9  TMEM owner and MMA issuer.
+namespace {
+constexpr int kWgThreads = 320;
+constexpr int kWgStages = 3;
+constexpr uint32_t kWgQ = kTlTile;                                  // after the keys
+constexpr uint32_t kWgPar = kWgQ + kWgStages * kTlTile;             // 4 slots x 128 rows x (factor, m, 1 / L, keys seen)
+constexpr uint32_t kWgSum = kWgPar + 4 * kTlRows * 16;              // 128 floats
+constexpr uint32_t kWgBar = kWgSum + 512;
+constexpr uint32_t kWgSmem = kWgBar + 256 + 1024;
+}  // namespace
+
+template <int FMT>
+__global__ void __launch_bounds__(kWgThreads, 1)
+    kv8_weigh_tile_kernel(const Kv8View c, const Kv8AttnArgs a, const float* w_in, float* w_out, int64_t w_seq,
+                          int64_t w_head) {
+  extern __shared__ unsigned char smem_dyn[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023u) & ~uintptr_t(1023u));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWgBar);
+  uint64_t* q_full = bars;          // [3] bulk copy
+  uint64_t* q_empty = bars + 3;     // [3] commit
+  uint64_t* par_full = bars + 6;    // [4] producer warp
+  uint64_t* s_full = bars + 10;     // [4] commit
+  uint64_t* s_empty = bars + 14;    // [4] 4 summing warps
+  uint64_t* drain = bars + 18;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 20);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.z, head = blockIdx.y, k0 = blockIdx.x * kTlKeys;
+  const int len = kv8_len(c, a, b);
+  if (k0 >= len) return;
+  // first item (256 query rows) of this sequence in the images: the items of the sequences in front of it
+  int item0 = 0;
+  for (int i = lane; i < b; i += 32) {
+    int x0, xn;
+    kv8_rows(a.cu, i, a.rows, x0, xn);
+    item0 += (int)(((int64_t)xn * a.group + 2 * kTlRows - 1) / (2 * kTlRows));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) item0 += __shfl_xor_sync(0xffffffffu, item0, off);
+  int r0, n;
+  kv8_rows(a.cu, b, a.rows, r0, n);
+  const int total = n * a.group;
+  const int i_first = a.causal ? max(0, k0 - (len - n)) : 0;          // first query token that sees key k0
+  const int tile0 = min(i_first, n) * a.group / kTlRows;
+  const int ntiles = (total + kTlRows - 1) / kTlRows;
+  const int cnt = max(0, ntiles - tile0);
+
+  if (tid == 0) {
+    for (int i = 0; i < kWgStages; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&par_full[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  // the block's keys: 128 tokens x 8 chunks
+  for (int e = tid; e < kTlKeys * 8; e += kWgThreads) {
+    const int t = e >> 3, ch = e & 7;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (k0 + t < len) {
+      const int page = kv8_page(c, b, (k0 + t) / kKv8Page);
+      if (page >= 0) w = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, page, head, 0) + kv8_chunk(t & 63, ch));
+    }
+    store_codes<FMT>(smem, t, ch, w);
+  }
+  fence_async_shared();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == 8) {
+    bool ok = true;
+    for (int i = 0; i < cnt && ok; ++i) {
+      const int qt = tile0 + i;
+      const int64_t img = ((int64_t)head * a.items + item0 + (qt >> 1)) * 2 + (qt & 1);
+      const int st = i % kWgStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[st], ((i / kWgStages) & 1) ^ 1))) { ok = false; break; }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[st], kTlTile);
+        bulk_load(smem + kWgQ + st * kTlTile, a.q_image + img * kTlTile, kTlTile, &q_full[st]);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_empty[i & 3], ((i >> 2) & 1) ^ 1))) { ok = false; break; }
+      float4* par = reinterpret_cast<float4*>(smem + kWgPar + (i & 3) * kTlRows * 16);
+      for (int x = lane; x < kTlRows; x += 32) {
+        const int rr = qt * kTlRows + x;
+        float4 v = make_float4(0.f, 0.f, 0.f, __int_as_float(0));
+        if (rr < total) {
+          const float2 s = a.stats[(int64_t)(r0 + rr / a.group) * a.q_heads + head * a.group + rr % a.group];
+          v = make_float4(a.q_coef[img * kTlRows + x], s.x, s.y,
+                          __int_as_float(kv8_visible(a.causal, len, n, rr / a.group)));
+        }
+        par[x] = v;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&par_full[i & 3]);
+    }
+    if (!ok) {   // copies still in flight land in this block's shared memory
+      const uint64_t t = globaltimer_ns();
+      while (globaltimer_ns() - t < 200000ull) {}
+    }
+  } else if (warp == 9) {
+    if (elect_one()) {
+      const uint32_t id = idesc_f16(kTlKeys, kTlRows);
+      const uint32_t kb = smem_u32(smem);
+      bool ok = true;
+      for (int i = 0; i < cnt && ok; ++i) {
+        const int st = i % kWgStages;
+        if (!mbar_wait(&q_full[st], (i / kWgStages) & 1) || !mbar_wait(&s_empty[i & 3], ((i >> 2) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t qb = smem_u32(smem + kWgQ + st * kTlTile);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
+          mma_bf16_ss(tmem + (i & 3) * 128, smem_desc_kmajor(kb + off, 128), smem_desc_kmajor(qb + off, 128), id, kk > 0);
+        }
+        tc_commit(&s_full[i & 3]);
+        tc_commit(&q_empty[st]);
+      }
+      tc_commit(drain);
+      mbar_wait(drain, 0, 100000000ull);
+    }
+    __syncwarp();
+  }
+  float acc = 0.f;
+  bool ok = true;
+  if (warp < 8) {
+    const int key = k0 + 32 * (warp & 3) + lane;
+    float sk = 1.f;
+    if (key < len) {
+      const int page = kv8_page(c, b, key / kKv8Page);
+      if (page >= 0) sk = c.scales[kv8_scale(c, page, head, 0)];
+    }
+    const uint32_t lane_addr = (32u * (uint32_t)(warp & 3)) << 16;
+    for (int i = warp >> 2; i < cnt; i += 2) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&par_full[i & 3], (i >> 2) & 1) && mbar_wait(&s_full[i & 3], (i >> 2) & 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float4* par = reinterpret_cast<const float4*>(smem + kWgPar + (i & 3) * kTlRows * 16);
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t s[32];
+        tmem_ld32(tmem + lane_addr + (i & 3) * 128 + 32 * q, s);
+        tmem_wait_ld();
+        tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(s));
+        tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(s + 16));
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float4 v = par[32 * q + e];
+          const float p = ex2(fmaf(__uint_as_float(s[e]) * sk, v.x, -v.y)) * v.z;
+          part[e & 3] += key < __float_as_int(v.w) ? p : 0.f;
+        }
+      }
+      acc += (part[0] + part[1]) + (part[2] + part[3]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_empty[i & 3]);
+    }
+    if (warp >= 4) reinterpret_cast<float*>(smem + kWgSum)[tid - 128] = acc;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp < 4 && ok && k0 + tid < len) {
+    const int64_t at = b * w_seq + head * w_head + k0 + tid;
+    w_out[at] = w_in[at] + (acc + reinterpret_cast<const float*>(smem + kWgSum)[tid]);
+  }
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host launchers
+// ---------------------------------------------------------------------------
+// How a call runs, from its sizes alone (the workspace is sized by the same rule).
+struct Kv8Plan {
+  bool stream;
+  int items, nsplit;
+  int64_t part_o, part_ml, stats, logits, q_image, q_coef, bytes;   // workspace offsets, -1 for none
+  int64_t logit_ld;
+};
+
+// Query rows that share a key/value head, per sequence, up to which the streaming kernel runs.
+constexpr int kStreamRows = 32;
+
+Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool weigh) {
+  Kv8Plan p{};
+  const int group = q_heads / heads;
+  const int64_t packed = (int64_t)rows * group;
+  p.stream = packed <= (int64_t)kStreamRows * seqs;
+  const int unit = p.stream ? kStRows : 2 * kTlRows;
+  const int busy = std::min(seqs, rows);             // sequences that can have queries
+  p.items = (int)std::min<int64_t>(packed, packed / unit + busy);
+  const int64_t blocks = (int64_t)p.items * heads;
+  const int target = 148 * 4;
+  const int steps = std::max(1, (max_len + kTlKeys - 1) / kTlKeys);
+  // a split is worth its partial result when it has a few steps of its own
+  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({(target + blocks - 1) / blocks, steps / 4, 64}));
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  const int64_t fr = (int64_t)rows * q_heads;
+  p.part_o = p.nsplit > 1 ? take(fr * p.nsplit * kKv8Dim * 4) : -1;
+  p.part_ml = p.nsplit > 1 ? take(fr * p.nsplit * 8) : -1;
+  p.stats = weigh ? take(fr * 8) : -1;
+  p.logit_ld = (max_len + kKv8Page - 1) / kKv8Page * (int64_t)kKv8Page;
+  p.logits = weigh && p.stream ? take(fr * p.logit_ld * 4) : -1;
+  p.q_image = weigh && !p.stream ? take((int64_t)heads * p.items * 2 * kTlTile) : -1;
+  p.q_coef = weigh && !p.stream ? take((int64_t)heads * p.items * 2 * kTlRows * 4) : -1;
+  p.bytes = at;
+  return p;
+}
+
+int64_t kv8_attn_workspace_bytes(int seqs, int heads, int q_heads, int rows, int max_len, bool weigh) {
+  return kv8_plan(seqs, heads, q_heads, rows, max_len, weigh).bytes;
+}
+
+namespace {
+template <int FMT>
+cudaError_t launch_kv8_attn_fmt(const Kv8View& c, const Kv8AttnArgs& a, const Kv8Plan& p, const float* w_in,
+                                float* w_out, int64_t w_seq, int64_t w_head, cudaStream_t st) {
+  cudaError_t e;
+  if (a.rows > 0) {
+    const dim3 grid(p.items, c.heads, p.nsplit);
+    if (p.stream) {
+      e = cudaFuncSetAttribute(kv8_stream_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStSmem);
+      if (e != cudaSuccess) return e;
+      kv8_stream_kernel<FMT><<<grid, kStThreads, kStSmem, st>>>(c, a);
+    } else {
+      e = cudaFuncSetAttribute(kv8_tile_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTlSmem);
+      if (e != cudaSuccess) return e;
+      kv8_tile_kernel<FMT><<<grid, kTlThreads, kTlSmem, st>>>(c, a);
+    }
+    if (p.nsplit > 1) {
+      const int64_t fr = (int64_t)a.rows * a.q_heads;
+      kv8_combine_kernel<<<(unsigned)((fr + 7) / 8), 256, 0, st>>>(a);
+    }
+  }
+  if (w_out && a.max_len > 0) {
+    if (p.stream) {
+      kv8_weigh_logits_kernel<<<dim3((a.max_len + 255) / 256, c.heads, c.seqs), 256, 0, st>>>(c, a, w_in, w_out, w_seq,
+                                                                                              w_head);
+    } else {
+      e = cudaFuncSetAttribute(kv8_weigh_tile_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWgSmem);
+      if (e != cudaSuccess) return e;
+      kv8_weigh_tile_kernel<FMT><<<dim3((a.max_len + kTlKeys - 1) / kTlKeys, c.heads, c.seqs), kWgThreads, kWgSmem,
+                                   st>>>(c, a, w_in, w_out, w_seq, w_head);
+    }
+  }
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_kv8_attn(const Kv8View& c, bool e4m3, const int32_t* lens, const int32_t* cu, const uint16_t* q,
+                            int64_t ldq, int rows, int q_heads, bool causal, float scale_log2, int max_len,
+                            uint16_t* o, int64_t ldo, const float* w_in, float* w_out, int64_t w_seq, int64_t w_head,
+                            void* work, cudaStream_t st) {
+  const Kv8Plan p = kv8_plan(c.seqs, c.heads, q_heads, rows, max_len, w_out != nullptr);
+  uint8_t* ws = static_cast<uint8_t*>(work);
+  auto at = [&](int64_t off) { return off < 0 ? nullptr : ws + off; };
+  Kv8AttnArgs a{};
+  a.q = q;
+  a.ldq = ldq;
+  a.o = o;
+  a.ldo = ldo;
+  a.cu = cu;
+  a.lens = lens;
+  a.rows = rows;
+  a.q_heads = q_heads;
+  a.group = q_heads / c.heads;
+  a.causal = causal;
+  a.seqs = c.seqs;
+  a.max_len = max_len;
+  a.nsplit = p.nsplit;
+  a.items = p.items;
+  a.scale_log2 = scale_log2;
+  a.part_o = reinterpret_cast<float*>(at(p.part_o));
+  a.part_ml = reinterpret_cast<float2*>(at(p.part_ml));
+  a.stats = reinterpret_cast<float2*>(at(p.stats));
+  a.logits = reinterpret_cast<float*>(at(p.logits));
+  a.logit_ld = p.logit_ld;
+  a.q_image = at(p.q_image);
+  a.q_coef = reinterpret_cast<float*>(at(p.q_coef));
+  return e4m3 ? launch_kv8_attn_fmt<RBD_CODES_E4M3>(c, a, p, w_in, w_out, w_seq, w_head, st)
+              : launch_kv8_attn_fmt<RBD_CODES_INT8>(c, a, p, w_in, w_out, w_seq, w_head, st);
+}
+
+}  // namespace rbd

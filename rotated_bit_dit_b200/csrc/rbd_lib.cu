@@ -9,4 +9,7 @@
 #include "rbd_kv4.cu"
 #include "rbd_rope.cu"
 #include "rbd_attn.cu"
+#include "rbd_kv8.cu"
+#include "rbd_kv8_attn.cu"
+#include "rbd_kv8_tile.cu"
 #include "rbd_svdquant.cu"
