@@ -467,7 +467,7 @@ typedef struct rbd_kv8 {
 /* Append: tokens lens[b] .. lens[b] + n - 1 of sequence b from its n rows of
  * k, v (bf16 [rows, ld], head h at h * 128; ld >= 128 heads, ld % 8 == 0,
  * 16-byte aligned).  lens is not changed.  Per (page, head, side), float32:
- *   s = max(s_old, RN(amax / qmax), 2^-100), code = round(RN(x * RN(1 / s))),
+ *   s = max(s_old, RN(amax * RN(1 / qmax)), 2^-100), code = round(RN(x * RN(1 / s))),
  * qmax 127 (INT8: nearest whole number, ties to even, within -127 .. 127) or 448
  * (E4M3: nearest value, ties to even, saturating); amax over the finite new
  * values of the page; s_old the page's scale if it held tokens, whose codes are

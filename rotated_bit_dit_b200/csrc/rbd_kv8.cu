@@ -2,7 +2,7 @@
 // accumulated attention weight.  The attention over it is in rbd_kv8_attn.cu.
 //
 // Quantisation of a page, per head and side, over its 64 x 128 values:
-//   s = max(s_old, RN(amax / qmax), 2^-100),  inv = RN(1 / s),
+//   s = max(s_old, RN(amax * RN(1 / qmax)), 2^-100),  inv = RN(1 / s),
 //   code = round(RN(x * inv))  (to the nearest whole number in [-127, 127], or E4M3 value, ties to even)
 // with qmax = 127 (INT8) or 448 (E4M3), amax over the finite values that join
 // the page, and s_old the page's scale while it already holds tokens.  When the
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(256)
   __syncthreads();
   m = max(max(red[side][0], red[side][1]), max(red[side][2], red[side][3]));
   const float amax = __uint_as_float(m << 16);
-  const float s = fmaxf(fmaxf(s_old, __fdiv_rn(amax, kv8_qmax<FMT>())), kKv8Floor);
+  const float s = fmaxf(fmaxf(s_old, __fmul_rn(amax, kv8_inv_qmax<FMT>())), kKv8Floor);
   const float inv = __frcp_rn(s);
   uint8_t* tile = c.codes + kv8_tile(c, page, head, side);
 #pragma unroll
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(256)
   if ((tid & 31) == 0) red[side][tid >> 5] = m_bits;
   __syncthreads();
   am = __uint_as_float(max(max(red[side][0], red[side][1]), max(red[side][2], red[side][3])));
-  const float s = fmaxf(__fdiv_rn(am, kv8_qmax<FMT>()), kKv8Floor);
+  const float s = fmaxf(__fmul_rn(am, kv8_inv_qmax<FMT>()), kKv8Floor);
   const float inv = __frcp_rn(s);
   uint8_t* tile = c.codes + kv8_tile(c, dst_page, head, side);
 #pragma unroll

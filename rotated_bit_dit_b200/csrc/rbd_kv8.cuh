@@ -95,7 +95,9 @@ __device__ __forceinline__ bool kv8_find(int seqs, int x, Count count, int& b, i
 }
 
 template <int FMT>
-__host__ __device__ __forceinline__ constexpr float kv8_qmax() { return FMT == RBD_CODES_INT8 ? 127.f : 448.f; }
+__host__ __device__ __forceinline__ constexpr float kv8_inv_qmax() {
+  return FMT == RBD_CODES_INT8 ? 1.f / 127.f : 1.f / 448.f;
+}
 
 // Code of x under the inverse scale inv; a NaN is stored as zero, an infinity as the largest code.
 template <int FMT>

@@ -5,7 +5,7 @@ import numpy as np
 
 PAGE, DIM = 64, 128
 FLOOR = np.float32(2.0 ** -100)
-QMAX = {0: np.float32(127), 1: np.float32(448)}
+INV_QMAX = {0: np.float32(1) / np.float32(127), 1: np.float32(1) / np.float32(448)}
 
 
 def e4m3(y):
@@ -44,7 +44,7 @@ class PlainCache:
                     at = codes.shape[0]
                     part, x = x[:PAGE - at % PAGE], x[PAGE - at % PAGE:]
                     fin = np.abs(part[np.isfinite(part)])
-                    s = np.float32(max(np.float32(fin.max(initial=0.0)) / QMAX[self.fmt], FLOOR))
+                    s = np.float32(max(np.float32(fin.max(initial=0.0)) * INV_QMAX[self.fmt], FLOOR))
                     if at % PAGE:
                         old = scales[-1]
                         s = np.float32(max(s, old))
@@ -117,7 +117,7 @@ class PlainCache:
                 codes, scales = [], []
                 for a in range(0, val.shape[0], PAGE):
                     part = val[a:a + PAGE]
-                    sc = np.float32(max(np.abs(part).max(initial=0.0) / QMAX[self.fmt], FLOOR))
+                    sc = np.float32(max(np.abs(part).max(initial=0.0) * INV_QMAX[self.fmt], FLOOR))
                     scales.append(sc)
                     codes.append(quantise(part, np.float32(1) / sc, self.fmt))
                 self.codes[b][h][side] = np.concatenate(codes) if codes else np.zeros((0, DIM), np.float32)
