@@ -49,6 +49,9 @@ struct Kv8AttnArgs {
   int64_t logit_ld;
   uint8_t* q_image;    // [heads][items][2][32 KB]: the fp16 query tiles (tile kernel), or null
   float* q_coef;       // [heads][items][2][128]: base-2 score factor of every row of them
+  uint8_t* kv_image;   // [seqs][image_steps][heads][2][32 KB]: fp16 operands of every 128-key step, or null
+  float4* kv_scale;    // [seqs][image_steps][heads][2]: their page scales (s_k, log2 s_v, 1 / s_v, -)
+  int image_steps;
 };
 
 namespace {

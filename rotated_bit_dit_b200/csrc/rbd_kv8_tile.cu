@@ -3,19 +3,26 @@
 // scaling) is described in rbd_kv8_attn.cu.
 //
 // kv8_tile_kernel, one block per 256 rows (two query tiles of 128) of one
-// (sequence, key/value head) and one split of its keys; four warpgroups:
-//   0, 1   softmax of query tile 0 / 1, one row per thread (TMEM lane = row);
-//   2      converters: codes from global memory to fp16 operands in shared memory;
-//   3      one warp: TMEM owner and MMA issuer.
-// Per 128-key step (two pages) and query tile t: S_t = Q_t K^T into TMEM columns
-// 128 t .. (fp16 operands from shared memory), the softmax writes P_t as fp16 over
-// the first 64 of those columns, and O_t += P_t V takes P_t from TMEM and V from
-// shared memory as it is stored, token by token (an MN-major operand), so V is
-// never transposed.  The issuer interleaves the tiles: while softmax t works, the
-// tensor core runs P.V and Q.K^T of the other tile.
-// Converting inside the kernel keeps global traffic at one byte per value and puts
-// the work on warps that have issue slots to spare: a 128-key step is 32 KB of
-// codes for 16.8 MFLOP.
+// (sequence, key/value head) and one split of its keys:
+//   warps 0-7, 8-15  softmax of query tile 0 / 1: TMEM lane = row, two threads a
+//                    row, each with one page (64 keys) of a 128-key step;
+//   warp 16          TMEM owner and MMA issuer;
+//   warp 17          loader of prepared operands (a bulk copy each), or
+//   warps 20-23      converters: codes from global memory to fp16 operands.
+// Per step and query tile t: S_t = Q_t K^T into TMEM columns 128 t .. (fp16 operands
+// from shared memory), the softmax writes P_t as fp16 over the first 64 of those
+// columns, and O_t += P_t V takes P_t from TMEM and V from shared memory as it is
+// stored, token by token (an MN-major operand), so V is never transposed.  The
+// issuer interleaves the tiles: while softmax t works, the tensor core runs P.V and
+// Q.K^T of the other tile.
+// Operands come in one of two ways.  Where a key is used by several blocks (prompts,
+// image blocks), kv8_prepare_kernel converts every step's codes once into operand
+// images in the workspace; converting in every block cost the softmax its integer
+// pipe (4096 queries over 16384 keys x 24 heads: 2157 us against 748 without softmax
+// and converters).  Where it is used once, the images' traffic (5 bytes a value
+// against 1) would dominate, and the block converts for itself.
+#include <type_traits>
+
 #include "rbd_kv8.cuh"
 #include "rbd_internal.cuh"
 
@@ -25,14 +32,26 @@ namespace {
 
 constexpr int kTlRows = 128;                       // rows of a query tile (TMEM lanes)
 constexpr int kTlKeys = 128;                       // keys per step
-constexpr int kTlThreads = 512;
+constexpr int kTlThreads = 640;                    // with a loader
+constexpr int kTlConvThreads = 768;                // with converters
 constexpr uint32_t kTlTile = 32768;                // a 128 x 128 fp16 operand: two 64-channel halves of 128-byte rows
 constexpr uint32_t kTlK = 2 * kTlTile;             // keys, 2 stages
 constexpr uint32_t kTlV = kTlK + 2 * kTlTile;      // values, 2 stages
 constexpr uint32_t kTlScale = kTlV + 2 * kTlTile;  // page scales: 4 slots x 2 pages x (s_k, log2 s_v, 1 / s_v, -)
 constexpr uint32_t kTlCoef = kTlScale + 4 * 32;    // base-2 score factor of the 256 rows
-constexpr uint32_t kTlBar = kTlCoef + 256 * 4;
+constexpr uint32_t kTlRed = kTlCoef + 256 * 4;     // row maxima (then sums): 2 buffers x 2 tiles x 2 halves x 128 rows
+constexpr uint32_t kTlBar = kTlRed + 2 * 2 * 2 * 128 * 4;
 constexpr uint32_t kTlSmem = kTlBar + 256 + 1024;  // + alignment slack
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// The larger of three (one instruction on sm_100).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // Shared-memory descriptor of an MN-major fp16 operand with the 128-byte swizzle: rows of 64 MN elements (128
 // bytes), one row per K index; 8-row groups sbo bytes apart along K, 64-element blocks lbo bytes apart along MN.
@@ -81,18 +100,57 @@ __device__ __forceinline__ void store_codes(unsigned char* tile, int t, int c, c
 
 }  // namespace
 
+// Operand images of every 128-key step of the sequences: [seqs][steps][heads] x (32
+// KB of keys, 32 KB of values, as the tensor core reads them) and the page scales.
 template <int FMT>
-__global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c, const Kv8AttnArgs a) {
+__global__ void __launch_bounds__(256)
+    kv8_prepare_kernel(const Kv8View c, const Kv8AttnArgs a) {
+  const int b = blockIdx.z, head = blockIdx.y, step = blockIdx.x;
+  const int len = kv8_len(c, a, b);
+  if (step * kTlKeys >= len) return;
+  const int64_t img = ((int64_t)b * gridDim.x + step) * c.heads + head;
+  int page[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int p = 2 * step + h;
+    page[h] = p * kKv8Page < len ? kv8_page(c, b, p) : -1;
+  }
+  if (threadIdx.x < 2) {
+    float2 sc = make_float2(1.f, 1.f);
+    if (page[threadIdx.x] >= 0)
+      sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page[threadIdx.x], head, 0));
+    a.kv_scale[img * 2 + threadIdx.x] = make_float4(sc.x, log2f(sc.y), 1.0f / sc.y, 0.f);
+  }
+  uint4 raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = threadIdx.x + 256 * (i & 3);
+    const int t = e >> 3, ch = e & 7, side = i >> 2;
+    const int pg = page[t >> 6];
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (pg >= 0 && step * kTlKeys + t < len)
+      raw[i] = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, pg, head, side) + kv8_chunk(t & 63, ch));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = threadIdx.x + 256 * (i & 3);
+    store_codes<FMT>(a.kv_image + img * 2 * kTlTile + (i >> 2) * kTlTile, e >> 3, e & 7, raw[i]);
+  }
+}
+
+template <int FMT, bool CONV>
+__global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
+    kv8_tile_kernel(const Kv8View c, const Kv8AttnArgs a) {
   extern __shared__ unsigned char smem_dyn[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023u) & ~uintptr_t(1023u));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kTlBar);
-  uint64_t* k_full = bars;          // [2] 4 converter warps
+  uint64_t* k_full = bars;          // [2] bulk copies, or 4 converter warps
   uint64_t* k_empty = bars + 2;     // [2] commit
   uint64_t* v_full = bars + 4;      // [2]
   uint64_t* v_empty = bars + 6;     // [2]
   uint64_t* s_full = bars + 8;      // [2] per query tile, commit
-  uint64_t* p_full = bars + 10;     // [2] per query tile, 4 softmax warps
+  uint64_t* p_full = bars + 10;     // [2] per query tile, 8 softmax warps
   uint64_t* sc_full = bars + 12;    // [4] the two page scales of a step
   uint64_t* o_done = bars + 16;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 18);
@@ -133,24 +191,24 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 4);
+      mbar_init(&k_full[i], CONV ? 4 : 1);
       mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 4);
+      mbar_init(&v_full[i], CONV ? 4 : 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sc_full[i], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&sc_full[i], CONV ? 2 : 1);
     mbar_init(o_done, 1);
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
     tc_fence_before();
   }
   // Queries: bf16 rows to fp16 tiles, 16 lanes a row
-  for (int r = warp * 2 + (lane >> 4); r < 2 * kTlRows; r += 32) {
+  for (int r = warp * 2 + (lane >> 4); r < 2 * kTlRows; r += (CONV ? kTlConvThreads : kTlThreads) / 16) {
     const int ch = lane & 15;
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     if (r < nrows) {
@@ -162,8 +220,10 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
     uint32_t amax = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) amax = max(amax, max(ws[e] & 0x7FFFu, (ws[e] >> 16) & 0x7FFFu));
+    // (the 16 lanes of a row leave the loop together)
+    const uint32_t half_mask = lane < 16 ? 0x0000FFFFu : 0xFFFF0000u;
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    for (int off = 8; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(half_mask, amax, off));
     float f, inv;
     kv8_row_scale(amax, f, inv);
     uint32_t h[4];
@@ -185,10 +245,64 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp >= 12) {
-    // ------------------------------------------------------------ MMA issuer
-    reg_dec<40>();
-    if (warp == 12 && elect_one() && cnt > 0) {
+  if (warp >= 20) {
+    // ------------------------------------------------------------ converters
+    // a warp takes 32 tokens of a step (half a page); a lane, 16 channels of 8 of them
+    if (CONV) {
+      reg_inc<88>();
+      const int w4 = warp - 20;
+      uint4 raw[8];
+      float2 sc = make_float2(1.f, 1.f);
+      auto fetch = [&](int side, int j) {
+        const int p = (j0 + j) * 2 + (w4 >> 1);
+        const int held = len - p * kKv8Page;                     // tokens of the page
+        const int page = held > 0 ? kv8_page(c, b, p) : -1;
+        const uint8_t* src = page >= 0 ? c.codes + kv8_tile(c, page, head, side) : nullptr;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 32 * (w4 & 1) + 8 * (i >> 1) + (lane >> 2);
+          const int ch = (lane & 3) + 4 * (i & 1);
+          raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (src && row < held) raw[i] = *reinterpret_cast<const uint4*>(src + kv8_chunk(row, ch));
+        }
+        if (side == 0) {
+          sc = make_float2(1.f, 1.f);
+          if (page >= 0) sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page, head, 0));
+        }
+      };
+      auto put = [&](int side, int j) {
+        unsigned char* dst = smem + (side ? kTlV : kTlK) + (j & 1) * kTlTile;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          store_codes<FMT>(dst, 32 * w4 + 8 * (i >> 1) + (lane >> 2), (lane & 3) + 4 * (i & 1), raw[i]);
+      };
+      if (cnt > 0) fetch(0, 0);
+      for (int j = 0; j < cnt; ++j) {
+        const uint32_t par = ((j >> 1) & 1) ^ 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[j & 1], par))) break;
+        put(0, j);
+        // Slot j % 4 was last read for step j - 4, whose P V (awaited before its K stage came free for step j - 2)
+        // follows that softmax.
+        if ((w4 & 1) == 0 && lane == 0)
+          *reinterpret_cast<float4*>(smem + kTlScale + (j & 3) * 32 + (w4 >> 1) * 16) =
+              make_float4(sc.x, log2f(sc.y), 1.0f / sc.y, 0.f);
+        fetch(1, j);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[j & 1]);
+        if ((w4 & 1) == 0 && lane == 0) mbar_arrive(&sc_full[j & 3]);
+        if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[j & 1], par))) break;
+        put(1, j);
+        if (j + 1 < cnt) fetch(0, j + 1);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[j & 1]);
+      }
+    }
+  } else if (warp >= 16) {
+    reg_dec<CONV ? 40 : 64>();
+    if (warp == 16 && elect_one() && cnt > 0) {
+      // ------------------------------------------------------------ MMA issuer
       const uint32_t id_qk = idesc_f16(kTlRows, kTlKeys);
       const uint32_t id_pv = idesc_f16(kTlRows, kKv8Dim) | kIdescBMn;
       bool ok = true;
@@ -229,75 +343,48 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
       }
       tc_commit(o_done);
       mbar_wait(o_done, 0, 100000000ull);
+    } else if (!CONV && warp == 17 && lane == 0) {
+      // ------------------------------------------------------------ loader
+      bool ok = true;
+      for (int j = 0; j < cnt && ok; ++j) {
+        const int st = j & 1;
+        const uint32_t par = ((j >> 1) & 1) ^ 1;
+        const int64_t img = ((int64_t)b * a.image_steps + j0 + j) * c.heads + head;
+        const uint8_t* src = a.kv_image + img * 2 * kTlTile;
+        if (!mbar_wait(&k_empty[st], par)) { ok = false; break; }
+        mbar_arrive_expect_tx(&k_full[st], kTlTile);
+        bulk_load(smem + kTlK + st * kTlTile, src, kTlTile / 2, &k_full[st]);
+        bulk_load(smem + kTlK + st * kTlTile + kTlTile / 2, src + kTlTile / 2, kTlTile / 2, &k_full[st]);
+        // slot j % 4 was last read for step j - 4, whose P V (awaited before its K stage came free for step j - 2)
+        // follows that softmax
+        mbar_arrive_expect_tx(&sc_full[j & 3], 32);
+        bulk_load(smem + kTlScale + (j & 3) * 32, a.kv_scale + img * 2, 32, &sc_full[j & 3]);
+        if (!mbar_wait(&v_empty[st], par)) { ok = false; break; }
+        mbar_arrive_expect_tx(&v_full[st], kTlTile);
+        bulk_load(smem + kTlV + st * kTlTile, src + kTlTile, kTlTile / 2, &v_full[st]);
+        bulk_load(smem + kTlV + st * kTlTile + kTlTile / 2, src + kTlTile + kTlTile / 2, kTlTile / 2, &v_full[st]);
+      }
+      if (!ok) {   // copies still in flight land in this block's shared memory
+        const uint64_t t = globaltimer_ns();
+        while (globaltimer_ns() - t < 200000ull) {}
+      }
     }
     __syncwarp();
-  } else if (warp >= 8) {
-    // ------------------------------------------------------------ converters
-    // a warp takes 32 tokens of a step (half a page); a lane, 16 channels of 8 of them
-    reg_dec<104>();
-    const int w4 = warp - 8;
-    uint4 raw[2][8];
-    float2 sc = make_float2(1.f, 1.f);
-    auto fetch = [&](int side, int j) {
-      const int p = (j0 + j) * 2 + (w4 >> 1);
-      const int held = len - p * kKv8Page;                     // tokens of the page
-      const int page = held > 0 ? kv8_page(c, b, p) : -1;
-      const uint8_t* src = page >= 0 ? c.codes + kv8_tile(c, page, head, side) : nullptr;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = 32 * (w4 & 1) + 8 * (i >> 1) + (lane >> 2);
-        const int ch = (lane & 3) + 4 * (i & 1);
-        raw[side][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (src && row < held) raw[side][i] = *reinterpret_cast<const uint4*>(src + kv8_chunk(row, ch));
-      }
-      if (side == 0) {
-        sc = make_float2(1.f, 1.f);
-        if (page >= 0) sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page, head, 0));
-      }
-    };
-    auto put = [&](int side, int j) {
-      unsigned char* dst = smem + (side ? kTlV : kTlK) + (j & 1) * kTlTile;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        store_codes<FMT>(dst, 32 * w4 + 8 * (i >> 1) + (lane >> 2), (lane & 3) + 4 * (i & 1), raw[side][i]);
-    };
-    if (cnt > 0) {
-      fetch(0, 0);
-      fetch(1, 0);
-    }
-    for (int j = 0; j < cnt; ++j) {
-      const uint32_t par = ((j >> 1) & 1) ^ 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[j & 1], par))) break;
-      put(0, j);
-      // Slot j % 4 was last read for step j - 4, whose P V (awaited before its K stage came free for step j - 2)
-      // follows that softmax.
-      if ((w4 & 1) == 0 && lane == 0)
-        *reinterpret_cast<float4*>(smem + kTlScale + (j & 3) * 32 + (w4 >> 1) * 16) =
-            make_float4(sc.x, log2f(sc.y), 1.0f / sc.y, 0.f);
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[j & 1]);
-      if ((w4 & 1) == 0 && lane == 0) mbar_arrive(&sc_full[j & 3]);
-      if (j + 1 < cnt) fetch(0, j + 1);
-      if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[j & 1], par))) break;
-      put(1, j);
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full[j & 1]);
-      if (j + 1 < cnt) fetch(1, j + 1);
-    }
   } else {
     // ------------------------------------------------------------ softmax
-    reg_inc<184>();
-    const int t = warp >> 2;
-    const int r = tid;                                          // row of the block
+    reg_inc<CONV ? 88 : 104>();
+    const int t = warp >> 3, half = (warp >> 2) & 1;
+    const int tr = 32 * (warp & 3) + lane;                      // row of the tile (TMEM lane)
+    const int r = t * kTlRows + tr;                             // row of the block
     const bool live = r < nrows;
     const int rr = row_first + r;
     const int lim = live ? kv8_visible(a.causal, len, n, rr / a.group) : 0;
     const int min_lim = __reduce_min_sync(0xffffffffu, live ? lim : 0x7FFFFFFF);
     const float cq = coef[r];
     const uint32_t lane_addr = (32u * (uint32_t)(warp & 3)) << 16;
-    const uint32_t t_s = tmem + lane_addr + t * kTlKeys, t_o = tmem + lane_addr + 256 + t * kKv8Dim;
+    const uint32_t t_s = tmem + lane_addr + t * kTlKeys, t_o = tmem + lane_addr + 256 + t * kKv8Dim + 64 * half;
+    const int pair = 1 + t * 4 + (warp & 3);                    // named barrier of the two warps of these rows
+    float* red = reinterpret_cast<float*>(smem + kTlRed) + t * 256;
     auto wait_warp = [](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
     };
@@ -305,75 +392,81 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
     bool ok = true;
     const int mine = cnt_t[t];
     for (int j = 0; j < mine; ++j) {
-      if (!wait_warp(&sc_full[j & 3], (j >> 2) & 1) || !wait_warp(&s_full[t], j & 1)) { ok = false; break; }
+      // (a wait that gives up must not leave the other warp at the pair's barrier: it goes on, with nothing right)
+      ok = wait_warp(&sc_full[j & 3], (j >> 2) & 1) && ok;
+      ok = wait_warp(&s_full[t], j & 1) && ok;
       tc_fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, s + 32 * q);
-      const float4 sc0 = *reinterpret_cast<const float4*>(smem + kTlScale + (j & 3) * 32);
-      const float4 sc1 = *reinterpret_cast<const float4*>(smem + kTlScale + (j & 3) * 32 + 16);
+      uint32_t s[64];
+      tmem_ld32(t_s + 64 * half, s);
+      tmem_ld32(t_s + 64 * half + 32, s + 32);
+      const float4 sc = *reinterpret_cast<const float4*>(smem + kTlScale + (j & 3) * 32 + 16 * half);
+      const float cc = cq * sc.x;
+      const int k0 = (j0 + j) * kTlKeys + 64 * half;
+      const bool full = min_lim >= k0 + 64;                     // the warp's rows all see every key of the page
+      const int nv = lim - k0;
       tmem_wait_ld();
 #pragma unroll
-      for (int q = 0; q < 8; ++q) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(s + 16 * q));
-      const int k0 = (j0 + j) * kTlKeys;
-      const bool full = min_lim >= k0 + kTlKeys;                // the warp's rows all see every key of the step
-      const int nv = lim - k0;
+      for (int q = 0; q < 4; ++q) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(s + 16 * q));
       if (!full) {
 #pragma unroll
-        for (int e = 0; e < 128; ++e)
+        for (int e = 0; e < 64; ++e)
           if (e >= nv) s[e] = 0xFF800000u;                      // -inf
       }
-      float mx[8];
+      float mx[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(s[(e >> 2) * 64 + (e & 3)]);
+      for (int e = 0; e < 4; ++e) mx[e] = max3(__uint_as_float(s[e]), __uint_as_float(s[4 + e]), __uint_as_float(s[8 + e]));
 #pragma unroll
-      for (int e = 4; e < 64; ++e) {
-        mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
-        mx[4 + (e & 3)] = fmaxf(mx[4 + (e & 3)], __uint_as_float(s[64 + e]));
+      for (int e = 12; e < 60; e += 8) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], __uint_as_float(s[e + x]), __uint_as_float(s[e + 4 + x]));
       }
-      const float mx0 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const float mx1 = fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-      const float c0 = cq * sc0.x, c1 = cq * sc1.x;
-      const float mt = fmaxf(mx0 > -INFINITY ? fmaf(mx0, c0, sc0.y) : -INFINITY,
-                             mx1 > -INFINITY ? fmaf(mx1, c1, sc1.y) : -INFINITY);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(s[60 + x]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      float mt = top > -INFINITY ? fmaf(top, cc, sc.y) : -INFINITY;
+      float* ex = red + (j & 1) * 512 + tr;
+      ex[128 * half] = mt;
+      tc_fence_before();
+      bar_sync(pair, 64);      // both maxima are there, and both halves of S have been read
+      tc_fence_after();
+      mt = fmaxf(mt, ex[128 * (half ^ 1)]);
       const bool move = mt > m_run + kKv8Lazy;
       if (__any_sync(0xffffffffu, move)) {
         const float f = move ? ex2(m_run - mt) : 1.f;
         if (j > 0) {       // O holds steps 0 .. j - 1: their P V precede S of step j on the tensor core
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            uint32_t ov[32];
-            tmem_ld32(t_o + 32 * q, ov);
-            tmem_wait_ld();
+            uint32_t ov[16];
+            tmem_ld16(t_o + 16 * q, ov);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
-            tmem_st32(t_o + 32 * q, ov);
+            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+            tmem_st16(t_o + 16 * q, ov);
           }
           tmem_wait_st();
         }
         l_run *= f;
         if (move) m_run = mt;
       }
-      const float m_use = m_run > -INFINITY ? m_run : 0.f;
-      const float b0 = sc0.y - m_use, b1 = sc1.y - m_use;
-      float lp[4] = {0.f, 0.f, 0.f, 0.f};
+      const float bb = sc.y - (m_run > -INFINITY ? m_run : 0.f);
+      float lp[2] = {0.f, 0.f};
       // (a score factor of zero, from a vanishing query, would turn a masked -inf into a NaN: masked keys get p = 0)
+      auto probs = [&](auto all_seen) {
 #pragma unroll
-      for (int e = 0; e < 128; e += 2) {
-        const float cc = e < 64 ? c0 : c1, bb = e < 64 ? b0 : b1;
-        float x = ex2(fmaf(__uint_as_float(s[e]), cc, bb)), y = ex2(fmaf(__uint_as_float(s[e + 1]), cc, bb));
-        if (!full) {
-          x = e < nv ? x : 0.f;
-          y = e + 1 < nv ? y : 0.f;
+        for (int e = 0; e < 64; e += 2) {
+          float x = ex2(fmaf(__uint_as_float(s[e]), cc, bb)), y = ex2(fmaf(__uint_as_float(s[e + 1]), cc, bb));
+          if (!decltype(all_seen)::value) {
+            x = e < nv ? x : 0.f;
+            y = e + 1 < nv ? y : 0.f;
+          }
+          lp[0] += x;
+          lp[1] += y;
+          s[e >> 1] = half2_bits(x, y);
         }
-        lp[(e >> 6) * 2] += x;
-        lp[(e >> 6) * 2 + 1] += y;
-        s[e >> 1] = half2_bits(x, y);
-      }
-      l_run = fmaf(lp[0] + lp[1], sc0.z, l_run);
-      l_run = fmaf(lp[2] + lp[3], sc1.z, l_run);
-      tmem_st32(t_s, s);
-      tmem_st32(t_s + 32, s + 32);
+      };
+      if (full) probs(std::true_type{});
+      else probs(std::false_type{});
+      tmem_st32(t_s + 32 * half, s);
+      l_run = fmaf(lp[0] + lp[1], sc.z, l_run);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -381,7 +474,13 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
     }
     // output: O / L, or the split's O, m and L
     const bool have = mine > 0;
-    ok = ok && (cnt == 0 || wait_warp(o_done, 0));
+    {
+      float* ex = red + (mine & 1) * 512 + tr;
+      ex[128 * half] = l_run;
+      bar_sync(pair, 64);
+      l_run += ex[128 * (half ^ 1)];
+    }
+    ok = (cnt == 0 || wait_warp(o_done, 0)) && ok;
     tc_fence_after();
     if (ok) {
       const int qh = head * a.group + rr % a.group;
@@ -389,10 +488,12 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
       const int64_t fr = tok * a.q_heads + qh;
       const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
       const bool whole = a.nsplit == 1;
-      if (live && !whole) a.part_ml[fr * a.nsplit + split] = make_float2(m_run, l_run);
-      if (live && whole && a.stats) a.stats[fr] = make_float2(m_run > -INFINITY ? m_run : 0.f, inv);
+      if (live && half == 0) {
+        if (!whole) a.part_ml[fr * a.nsplit + split] = make_float2(m_run, l_run);
+        else if (a.stats) a.stats[fr] = make_float2(m_run > -INFINITY ? m_run : 0.f, inv);
+      }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 2; ++q) {
         uint32_t ov[32];
         if (have) {
           tmem_ld32(t_o + 32 * q, ov);
@@ -402,8 +503,9 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
           for (int e = 0; e < 32; ++e) ov[e] = 0u;
         }
         if (!live) continue;
+        const int d = 64 * half + 32 * q;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.o + tok * a.ldo + (int64_t)qh * kKv8Dim + 32 * q);
+          uint4* dst = reinterpret_cast<uint4*>(a.o + tok * a.ldo + (int64_t)qh * kKv8Dim + d);
 #pragma unroll
           for (int e8 = 0; e8 < 4; ++e8) {
             uint32_t w[4];
@@ -416,7 +518,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
             dst[e8] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (have) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + (fr * a.nsplit + split) * kKv8Dim + 32 * q);
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + (fr * a.nsplit + split) * kKv8Dim + d);
 #pragma unroll
           for (int e4 = 0; e4 < 8; ++e4) dst[e4] = make_uint4(ov[4 * e4], ov[4 * e4 + 1], ov[4 * e4 + 2], ov[4 * e4 + 3]);
         }
@@ -425,7 +527,7 @@ __global__ void __launch_bounds__(kTlThreads, 1) kv8_tile_kernel(const Kv8View c
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -634,12 +736,17 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 struct Kv8Plan {
   bool stream;
   int items, nsplit;
-  int64_t part_o, part_ml, stats, logits, q_image, q_coef, bytes;   // workspace offsets, -1 for none
+  bool prepare;        // operand images
+  int image_steps;     // 128-key steps of a sequence in them
+  int64_t part_o, part_ml, stats, logits, q_image, q_coef, kv_image, kv_scale, bytes;   // workspace offsets, -1 for none
   int64_t logit_ld;
 };
 
 // Query rows that share a key/value head, per sequence, up to which the streaming kernel runs.
 constexpr int kStreamRows = 32;
+// Operand images are made when a key is used by at least this many blocks on average, and fit in this much.
+constexpr int kPrepareItems = 3;
+constexpr int64_t kPrepareBytes = (int64_t)1 << 31;
 
 Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool weigh) {
   Kv8Plan p{};
@@ -654,6 +761,9 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   const int steps = std::max(1, (max_len + kTlKeys - 1) / kTlKeys);
   // a split is worth its partial result when it has a few steps of its own
   p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({(target + blocks - 1) / blocks, steps / 4, 64}));
+  p.image_steps = steps;
+  const int64_t images = (int64_t)seqs * steps * heads;
+  p.prepare = !p.stream && p.items >= kPrepareItems * (int64_t)busy && images * 2 * kTlTile <= kPrepareBytes;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -668,6 +778,8 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   p.logits = weigh && p.stream ? take(fr * p.logit_ld * 4) : -1;
   p.q_image = weigh && !p.stream ? take((int64_t)heads * p.items * 2 * kTlTile) : -1;
   p.q_coef = weigh && !p.stream ? take((int64_t)heads * p.items * 2 * kTlRows * 4) : -1;
+  p.kv_image = p.prepare ? take(images * 2 * kTlTile) : -1;
+  p.kv_scale = p.prepare ? take(images * 2 * 16) : -1;
   p.bytes = at;
   return p;
 }
@@ -688,9 +800,16 @@ cudaError_t launch_kv8_attn_fmt(const Kv8View& c, const Kv8AttnArgs& a, const Kv
       if (e != cudaSuccess) return e;
       kv8_stream_kernel<FMT><<<grid, kStThreads, kStSmem, st>>>(c, a);
     } else {
-      e = cudaFuncSetAttribute(kv8_tile_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTlSmem);
-      if (e != cudaSuccess) return e;
-      kv8_tile_kernel<FMT><<<grid, kTlThreads, kTlSmem, st>>>(c, a);
+      if (p.prepare) {
+        kv8_prepare_kernel<FMT><<<dim3(p.image_steps, c.heads, c.seqs), 256, 0, st>>>(c, a);
+        e = cudaFuncSetAttribute(kv8_tile_kernel<FMT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTlSmem);
+        if (e != cudaSuccess) return e;
+        kv8_tile_kernel<FMT, false><<<grid, kTlThreads, kTlSmem, st>>>(c, a);
+      } else {
+        e = cudaFuncSetAttribute(kv8_tile_kernel<FMT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTlSmem);
+        if (e != cudaSuccess) return e;
+        kv8_tile_kernel<FMT, true><<<grid, kTlConvThreads, kTlSmem, st>>>(c, a);
+      }
     }
     if (p.nsplit > 1) {
       const int64_t fr = (int64_t)a.rows * a.q_heads;
@@ -742,6 +861,9 @@ cudaError_t launch_kv8_attn(const Kv8View& c, bool e4m3, const int32_t* lens, co
   a.logit_ld = p.logit_ld;
   a.q_image = at(p.q_image);
   a.q_coef = reinterpret_cast<float*>(at(p.q_coef));
+  a.kv_image = at(p.kv_image);
+  a.kv_scale = reinterpret_cast<float4*>(at(p.kv_scale));
+  a.image_steps = p.image_steps;
   return e4m3 ? launch_kv8_attn_fmt<RBD_CODES_E4M3>(c, a, p, w_in, w_out, w_seq, w_head, st)
               : launch_kv8_attn_fmt<RBD_CODES_INT8>(c, a, p, w_in, w_out, w_seq, w_head, st);
 }

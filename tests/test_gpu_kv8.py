@@ -178,3 +178,15 @@ def test_weights(fmt, causal, held, new, heads, group):
     fill(cache, plain, rng, held)
     w = torch.from_numpy(rng.random((len(held), heads, 1601)).astype(np.float32)).cuda()
     check_attend(cache, plain, rng, new, heads * group, causal, q_gain=1.5, weights=w)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("held,new,heads,group", [([900], [800], 1, 1), ([700, 0, 333], [700, 50, 333], 2, 3),
+                                                  ([3000], [130], 1, 8), ([513, 64], [513, 512], 1, 2)])
+def test_attend_keys_shared_by_many_blocks(fmt, causal, held, new, heads, group):
+    rng = np.random.default_rng(sum(held) + 3 * sum(new))
+    cache, plain = R.Int8KVCache(len(held), 3180, heads, code_format=fmt), PlainCache(len(held), heads, fmt)
+    fill(cache, plain, rng, held)
+    w = torch.zeros((len(held), heads, 3200), device="cuda")
+    check_attend(cache, plain, rng, new, heads * group, causal, q_gain=1.5, weights=w)
