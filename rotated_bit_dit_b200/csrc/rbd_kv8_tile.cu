@@ -4,11 +4,10 @@
 //
 // kv8_tile_kernel, one block per 256 rows (two query tiles of 128) of one
 // (sequence, key/value head) and one split of its keys:
-//   warps 0-7, 8-15  softmax of query tile 0 / 1: TMEM lane = row, two threads a
-//                    row, each with one page (64 keys) of a 128-key step;
-//   warp 16          TMEM owner and MMA issuer;
-//   warp 17          loader of prepared operands (a bulk copy each), or
-//   warps 20-23      converters: codes from global memory to fp16 operands.
+//   warps 0-3, 4-7   softmax of query tile 0 / 1, a thread a row (TMEM lane);
+//   warp 8           TMEM owner and MMA issuer;
+//   warp 9           loader of prepared operands (a bulk copy each), or
+//   warps 12-15      converters: codes from global memory to fp16 operands.
 // Per step and query tile t: S_t = Q_t K^T into TMEM columns 128 t .. (fp16 operands
 // from shared memory), the softmax writes P_t as fp16 over the first 64 of those
 // columns, and O_t += P_t V takes P_t from TMEM and V from shared memory as it is
@@ -32,19 +31,54 @@ namespace {
 
 constexpr int kTlRows = 128;                       // rows of a query tile (TMEM lanes)
 constexpr int kTlKeys = 128;                       // keys per step
-constexpr int kTlThreads = 640;                    // with a loader
-constexpr int kTlConvThreads = 768;                // with converters
+constexpr int kTlThreads = 384;                    // with a loader
+constexpr int kTlConvThreads = 512;                // with converters
 constexpr uint32_t kTlTile = 32768;                // a 128 x 128 fp16 operand: two 64-channel halves of 128-byte rows
 constexpr uint32_t kTlK = 2 * kTlTile;             // keys, 2 stages
 constexpr uint32_t kTlV = kTlK + 2 * kTlTile;      // values, 2 stages
 constexpr uint32_t kTlScale = kTlV + 2 * kTlTile;  // page scales: 4 slots x 2 pages x (s_k, log2 s_v, 1 / s_v, -)
 constexpr uint32_t kTlCoef = kTlScale + 4 * 32;    // base-2 score factor of the 256 rows
-constexpr uint32_t kTlRed = kTlCoef + 256 * 4;     // row maxima (then sums): 2 buffers x 2 tiles x 2 halves x 128 rows
-constexpr uint32_t kTlBar = kTlRed + 2 * 2 * 2 * 128 * 4;
+constexpr uint32_t kTlBar = kTlCoef + 256 * 4;
 constexpr uint32_t kTlSmem = kTlBar + 256 + 1024;  // + alignment slack
 
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+// Two float32 operations in one issue slot: the softmax is short of slots, not of FMA lanes.
+__device__ __forceinline__ uint64_t pack_f32(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack_f32(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 2^x and 2^y on the FMA pipe, for a quarter of the keys: the special-function unit takes 8 cycles a warp for each
+// 2^x and is the longest phase of the softmax (1590 cycles of a 128-key step without this, 1275 with; 960 -> 922 us
+// at 4096 queries over 16384 keys x 24 heads; half of the keys: 985 us).  x = n + f with n the nearest whole number
+// and |f| <= 1/2; 2^f by its degree-4 polynomial of least largest relative error (2.6e-6, far under P's half step of
+// 2^-11); n added to the exponent.
+__device__ __forceinline__ void ex2_poly(float& x, float& y) {
+  const uint64_t v = pack_f32(fmaxf(x, -126.f), fmaxf(y, -126.f));
+  const uint64_t t = add_f32x2(v, pack_f32(12582912.f, 12582912.f));               // 1.5 * 2^23: rounds to whole
+  const uint64_t f = fma_f32x2(add_f32x2(t, pack_f32(-12582912.f, -12582912.f)), pack_f32(-1.f, -1.f), v);
+  uint64_t p = fma_f32x2(f, pack_f32(0.009570086374878883f, 0.009570086374878883f),
+                         pack_f32(0.055917851626873016f, 0.055917851626873016f));
+  p = fma_f32x2(f, p, pack_f32(0.240247443318367f, 0.240247443318367f));
+  p = fma_f32x2(f, p, pack_f32(0.6931217908859253f, 0.6931217908859253f));
+  p = fma_f32x2(f, p, pack_f32(0.9999992847442627f, 0.9999992847442627f));
+  float p0, p1, t0, t1;
+  unpack_f32(p, p0, p1);
+  unpack_f32(t, t0, t1);
+  x = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+  y = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 // The larger of three (one instruction on sm_100).
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -65,13 +99,32 @@ __device__ __forceinline__ uint64_t smem_desc_mnmajor(uint32_t smem_addr, uint32
   return d;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit float inputs, fp32 accumulation.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// The issuing warp runs its loop with all lanes, so that descriptors stay in uniform registers, and only the lane
+// with `leader` set issues: computed in one lane's branch they cost 90-115 cycles per product beside the softmax
+// warps, against 64 of the tensor core.
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit float inputs, fp32 accumulation.
+__device__ __forceinline__ void mma_f16_ss_if(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T.
+__device__ __forceinline__ void mma_f16_ts_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_if(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
       : "memory");
 }
 constexpr uint32_t kIdescBMn = 1u << 16;           // B is MN-major
@@ -86,16 +139,19 @@ __device__ __forceinline__ uint32_t tile_chunk(int t, int ch) {
   return (uint32_t)(ch >> 3) * 16384u + (uint32_t)t * 128u + (uint32_t)(((ch & 7) ^ (t & 7)) << 4);
 }
 
+// Eight codes as fp16, in order.
+template <int FMT>
+__device__ __forceinline__ uint4 eight_codes(const uint2& w) {
+  uint4 h;
+  kv8_to_f16<FMT>(FMT == RBD_CODES_INT8 ? prmt(w.x, 0u, 0x3120u) : w.x, h.x, h.y);
+  kv8_to_f16<FMT>(FMT == RBD_CODES_INT8 ? prmt(w.y, 0u, 0x3120u) : w.y, h.z, h.w);
+  return h;
+}
 // Sixteen codes of one token as fp16, channels 16 c .. 16 c + 15, into an operand tile.
 template <int FMT>
 __device__ __forceinline__ void store_codes(unsigned char* tile, int t, int c, const uint4& w) {
-  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    kv8_to_f16<FMT>(FMT == RBD_CODES_INT8 ? prmt(ws[i], 0u, 0x3120u) : ws[i], h[2 * i], h[2 * i + 1]);
-  *reinterpret_cast<uint4*>(tile + tile_chunk(t, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
-  *reinterpret_cast<uint4*>(tile + tile_chunk(t, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+  *reinterpret_cast<uint4*>(tile + tile_chunk(t, 2 * c)) = eight_codes<FMT>(make_uint2(w.x, w.y));
+  *reinterpret_cast<uint4*>(tile + tile_chunk(t, 2 * c + 1)) = eight_codes<FMT>(make_uint2(w.z, w.w));
 }
 
 }  // namespace
@@ -121,20 +177,23 @@ __global__ void __launch_bounds__(256)
       sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page[threadIdx.x], head, 0));
     a.kv_scale[img * 2 + threadIdx.x] = make_float4(sc.x, log2f(sc.y), 1.0f / sc.y, 0.f);
   }
-  uint4 raw[8];
+  // eight codes a thread and turn: 16 bytes out, whole 128-byte lines a warp
+  uint2 raw[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = threadIdx.x + 256 * (i & 3);
-    const int t = e >> 3, ch = e & 7, side = i >> 2;
+  for (int i = 0; i < 16; ++i) {
+    const int e = threadIdx.x + 256 * (i & 7);
+    const int t = e >> 4, ch = e & 15, side = i >> 3;
     const int pg = page[t >> 6];
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    raw[i] = make_uint2(0u, 0u);
     if (pg >= 0 && step * kTlKeys + t < len)
-      raw[i] = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, pg, head, side) + kv8_chunk(t & 63, ch));
+      raw[i] = *reinterpret_cast<const uint2*>(c.codes + kv8_tile(c, pg, head, side) + kv8_chunk(t & 63, ch >> 1) +
+                                               8 * (ch & 1));
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = threadIdx.x + 256 * (i & 3);
-    store_codes<FMT>(a.kv_image + img * 2 * kTlTile + (i >> 2) * kTlTile, e >> 3, e & 7, raw[i]);
+  for (int i = 0; i < 16; ++i) {
+    const int e = threadIdx.x + 256 * (i & 7);
+    *reinterpret_cast<uint4*>(a.kv_image + img * 2 * kTlTile + (i >> 3) * kTlTile + tile_chunk(e >> 4, e & 15)) =
+        eight_codes<FMT>(raw[i]);
   }
 }
 
@@ -145,15 +204,15 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023u) & ~uintptr_t(1023u));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kTlBar);
-  uint64_t* k_full = bars;          // [2] bulk copies, or 4 converter warps
+  uint64_t* k_full = bars;          // [2] keys and page scales: bulk copies, or 4 converter warps
   uint64_t* k_empty = bars + 2;     // [2] commit
   uint64_t* v_full = bars + 4;      // [2]
   uint64_t* v_empty = bars + 6;     // [2]
   uint64_t* s_full = bars + 8;      // [2] per query tile, commit
-  uint64_t* p_full = bars + 10;     // [2] per query tile, 8 softmax warps
-  uint64_t* sc_full = bars + 12;    // [4] the two page scales of a step
-  uint64_t* o_done = bars + 16;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 18);
+  uint64_t* p_full = bars + 10;     // [2] per query tile, 4 softmax warps
+  uint64_t* q_full = bars + 12;     // 8 softmax warps
+  uint64_t* o_done = bars + 13;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 14);
   float* coef = reinterpret_cast<float*>(smem + kTlCoef);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -196,61 +255,27 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
       mbar_init(&v_full[i], CONV ? 4 : 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 8);
+      mbar_init(&p_full[i], 4);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sc_full[i], CONV ? 2 : 1);
+    mbar_init(q_full, 8);
     mbar_init(o_done, 1);
     fence_barrier_init();
   }
-  if (warp == 16) {
+  if (warp == 8) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
     tc_fence_before();
   }
-  // Queries: bf16 rows to fp16 tiles, 16 lanes a row
-  for (int r = warp * 2 + (lane >> 4); r < 2 * kTlRows; r += (CONV ? kTlConvThreads : kTlThreads) / 16) {
-    const int ch = lane & 15;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (r < nrows) {
-      const int rr = row_first + r;
-      w = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(r0 + rr / a.group) * a.ldq +
-                                               (int64_t)(head * a.group + rr % a.group) * kKv8Dim + 8 * ch));
-    }
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-    uint32_t amax = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) amax = max(amax, max(ws[e] & 0x7FFFu, (ws[e] >> 16) & 0x7FFFu));
-    // (the 16 lanes of a row leave the loop together)
-    const uint32_t half_mask = lane < 16 ? 0x0000FFFFu : 0xFFFF0000u;
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(half_mask, amax, off));
-    float f, inv;
-    kv8_row_scale(amax, f, inv);
-    uint32_t h[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      h[e] = half2_bits(__uint_as_float(ws[e] << 16) * f, __uint_as_float(ws[e] & 0xFFFF0000u) * f);
-    const uint4 hv = make_uint4(h[0], h[1], h[2], h[3]);
-    const int t = r >> 7, tr = r & 127;
-    *reinterpret_cast<uint4*>(smem + t * kTlTile + tile_chunk(tr, ch)) = hv;
-    if (ch == 0) coef[r] = inv * a.scale_log2;
-    if (a.q_image && split == 0) {
-      const int64_t img = ((int64_t)head * a.items + item) * 2 + t;
-      *reinterpret_cast<uint4*>(a.q_image + img * kTlTile + tile_chunk(tr, ch)) = hv;
-      if (ch == 0) a.q_coef[img * kTlRows + tr] = inv * a.scale_log2;
-    }
-  }
-  fence_async_shared();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp >= 20) {
+  if (warp >= 12) {
     // ------------------------------------------------------------ converters
     // a warp takes 32 tokens of a step (half a page); a lane, 16 channels of 8 of them
     if (CONV) {
-      reg_inc<88>();
-      const int w4 = warp - 20;
+      reg_dec<104>();
+      const int w4 = warp - 12;
       uint4 raw[8];
       float2 sc = make_float2(1.f, 1.f);
       auto fetch = [&](int side, int j) {
@@ -290,7 +315,6 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[j & 1]);
-        if ((w4 & 1) == 0 && lane == 0) mbar_arrive(&sc_full[j & 3]);
         if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[j & 1], par))) break;
         put(1, j);
         if (j + 1 < cnt) fetch(0, j + 1);
@@ -299,51 +323,71 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
         if (lane == 0) mbar_arrive(&v_full[j & 1]);
       }
     }
-  } else if (warp >= 16) {
-    reg_dec<CONV ? 40 : 64>();
-    if (warp == 16 && elect_one() && cnt > 0) {
+  } else if (warp >= 8) {
+    reg_dec<CONV ? 40 : 56>();
+    if (warp == 8 && cnt > 0) {
       // ------------------------------------------------------------ MMA issuer
-      const uint32_t id_qk = idesc_f16(kTlRows, kTlKeys);
-      const uint32_t id_pv = idesc_f16(kTlRows, kKv8Dim) | kIdescBMn;
-      bool ok = true;
+      const uint32_t lead = elect_one();
+      constexpr uint32_t id_qk = idesc_f16(kTlRows, kTlKeys);
+      constexpr uint32_t id_pv = idesc_f16(kTlRows, kKv8Dim) | kIdescBMn;
+      const uint64_t q_desc = smem_desc_kmajor(smem_u32(smem), 128);
+      const uint64_t k_desc = smem_desc_kmajor(smem_u32(smem + kTlK), 128);
+      const uint64_t v_desc = smem_desc_mnmajor(smem_u32(smem + kTlV), 16384, 1024);
+      auto wait_warp = [](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+      };
       auto issue_qk = [&](int t, int j) {
-        const uint32_t qb = smem_u32(smem + t * kTlTile), kb = smem_u32(smem + kTlK + (j & 1) * kTlTile);
+        const uint64_t qd = q_desc + (uint32_t)t * (kTlTile >> 4), kd = k_desc + (uint32_t)(j & 1) * (kTlTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
-          mma_bf16_ss(tmem + t * kTlKeys, smem_desc_kmajor(qb + off, 128), smem_desc_kmajor(kb + off, 128), id_qk,
-                      kk > 0);
+          const uint32_t off = ((uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u) >> 4;
+          mma_f16_ss_if(lead, tmem + t * kTlKeys, qd + off, kd + off, id_qk, kk > 0);
         }
-        tc_commit(&s_full[t]);
+        tc_commit_if(lead, &s_full[t]);
       };
-      ok = mbar_wait(&k_full[0], 0);
+      // A wait costs about 100 cycles even when there is nothing to wait for, and the tensor core's queue is short:
+      // every wait stands behind eight products that are still running.
+      bool ok = wait_warp(q_full, 0) && wait_warp(&k_full[0], 0);
       if (ok) {
         tc_fence_after();
         for (int t = 0; t < 2; ++t)
           if (cnt_t[t] > 0) issue_qk(t, 0);
-        tc_commit(&k_empty[0]);
+        tc_commit_if(lead, &k_empty[0]);
+        ok = wait_warp(&v_full[0], 0);
       }
       for (int j = 0; j < cnt && ok; ++j) {
-        if (!mbar_wait(&v_full[j & 1], (j >> 1) & 1)) { ok = false; break; }
-        if (j + 1 < cnt && !mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) { ok = false; break; }
-        for (int t = 0; t < 2 && ok; ++t) {
+        const bool more = j + 1 < cnt;
+        bool k_ready = false, v_ready = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
           if (j >= cnt_t[t]) continue;
-          if (!mbar_wait(&p_full[t], j & 1)) { ok = false; break; }
+          if (!wait_warp(&p_full[t], j & 1)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t vb = smem_u32(smem + kTlV + (j & 1) * kTlTile);
+          const uint64_t vd = v_desc + (uint32_t)(j & 1) * (kTlTile >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts(tmem + 256 + t * kKv8Dim, tmem + t * kTlKeys + 8 * kk,
-                       smem_desc_mnmajor(vb + kk * 2048, 16384, 1024), id_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            mma_f16_ts_if(lead, tmem + 256 + t * kKv8Dim, tmem + t * kTlKeys + 8 * kk, vd + kk * (2048 >> 4), id_pv,
+                          (j > 0 || kk > 0) ? 1u : 0u);
+          if (more && !k_ready) {
+            if (!wait_warp(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) { ok = false; break; }
+            k_ready = true;
+            tc_fence_after();
+          } else if (more && !v_ready) {
+            if (!wait_warp(&v_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) { ok = false; break; }
+            v_ready = true;
+          }
           if (j + 1 < cnt_t[t]) issue_qk(t, j + 1);
         }
         if (!ok) break;
-        tc_commit(&v_empty[j & 1]);
-        if (j + 1 < cnt) tc_commit(&k_empty[(j + 1) & 1]);
+        tc_commit_if(lead, &v_empty[j & 1]);
+        if (more) {
+          tc_commit_if(lead, &k_empty[(j + 1) & 1]);
+          if (!v_ready && !wait_warp(&v_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) ok = false;
+        }
       }
-      tc_commit(o_done);
+      tc_commit_if(lead, o_done);
       mbar_wait(o_done, 0, 100000000ull);
-    } else if (!CONV && warp == 17 && lane == 0) {
+    } else if (!CONV && warp == 9 && lane == 0) {
       // ------------------------------------------------------------ loader
       bool ok = true;
       for (int j = 0; j < cnt && ok; ++j) {
@@ -352,13 +396,12 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
         const int64_t img = ((int64_t)b * a.image_steps + j0 + j) * c.heads + head;
         const uint8_t* src = a.kv_image + img * 2 * kTlTile;
         if (!mbar_wait(&k_empty[st], par)) { ok = false; break; }
-        mbar_arrive_expect_tx(&k_full[st], kTlTile);
+        // The page scales come with the keys, in slot j % 4: last read for step j - 4, whose P V (awaited before its
+        // K stage came free for step j - 2) follows that softmax.
+        mbar_arrive_expect_tx(&k_full[st], kTlTile + 32);
+        bulk_load(smem + kTlScale + (j & 3) * 32, a.kv_scale + img * 2, 32, &k_full[st]);
         bulk_load(smem + kTlK + st * kTlTile, src, kTlTile / 2, &k_full[st]);
         bulk_load(smem + kTlK + st * kTlTile + kTlTile / 2, src + kTlTile / 2, kTlTile / 2, &k_full[st]);
-        // slot j % 4 was last read for step j - 4, whose P V (awaited before its K stage came free for step j - 2)
-        // follows that softmax
-        mbar_arrive_expect_tx(&sc_full[j & 3], 32);
-        bulk_load(smem + kTlScale + (j & 3) * 32, a.kv_scale + img * 2, 32, &sc_full[j & 3]);
         if (!mbar_wait(&v_empty[st], par)) { ok = false; break; }
         mbar_arrive_expect_tx(&v_full[st], kTlTile);
         bulk_load(smem + kTlV + st * kTlTile, src + kTlTile, kTlTile / 2, &v_full[st]);
@@ -372,70 +415,110 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
-    reg_inc<CONV ? 88 : 104>();
-    const int t = warp >> 3, half = (warp >> 2) & 1;
-    const int tr = 32 * (warp & 3) + lane;                      // row of the tile (TMEM lane)
-    const int r = t * kTlRows + tr;                             // row of the block
+    reg_inc<CONV ? 184 : 224>();
+    // first the queries: bf16 rows to fp16 tiles, 16 lanes a row, a warp the 32 rows it will work on
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32; i0 += 16) {
+      const int ch = lane & 15;
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 32 * warp + i0 + 2 * i + (lane >> 4);
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < nrows) {
+          const int rr = row_first + r;
+          w[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(r0 + rr / a.group) * a.ldq +
+                                                      (int64_t)(head * a.group + rr % a.group) * kKv8Dim + 8 * ch));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 32 * warp + i0 + 2 * i + (lane >> 4);
+        const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t amax = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = max(amax, max(ws[e] & 0x7FFFu, (ws[e] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        float f, inv;
+        kv8_row_scale(amax, f, inv);
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h[e] = half2_bits(__uint_as_float(ws[e] << 16) * f, __uint_as_float(ws[e] & 0xFFFF0000u) * f);
+        const uint4 hv = make_uint4(h[0], h[1], h[2], h[3]);
+        const int qt = r >> 7, tr = r & 127;
+        *reinterpret_cast<uint4*>(smem + qt * kTlTile + tile_chunk(tr, ch)) = hv;
+        if (ch == 0) coef[r] = inv * a.scale_log2;
+        if (a.q_image && split == 0) {
+          const int64_t img = ((int64_t)head * a.items + item) * 2 + qt;
+          *reinterpret_cast<uint4*>(a.q_image + img * kTlTile + tile_chunk(tr, ch)) = hv;
+          if (ch == 0) a.q_coef[img * kTlRows + tr] = inv * a.scale_log2;
+        }
+      }
+    }
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+    const int t = warp >> 2;
+    const int r = tid;                                          // row of the block
     const bool live = r < nrows;
     const int rr = row_first + r;
     const int lim = live ? kv8_visible(a.causal, len, n, rr / a.group) : 0;
     const int min_lim = __reduce_min_sync(0xffffffffu, live ? lim : 0x7FFFFFFF);
     const float cq = coef[r];
     const uint32_t lane_addr = (32u * (uint32_t)(warp & 3)) << 16;
-    const uint32_t t_s = tmem + lane_addr + t * kTlKeys, t_o = tmem + lane_addr + 256 + t * kKv8Dim + 64 * half;
-    const int pair = 1 + t * 4 + (warp & 3);                    // named barrier of the two warps of these rows
-    float* red = reinterpret_cast<float*>(smem + kTlRed) + t * 256;
+    const uint32_t t_s = tmem + lane_addr + t * kTlKeys, t_o = tmem + lane_addr + 256 + t * kKv8Dim;
     auto wait_warp = [](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
     };
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
-    const int mine = cnt_t[t];
+    const int mine = t ? cnt_t[1] : cnt_t[0];
     for (int j = 0; j < mine; ++j) {
-      // (a wait that gives up must not leave the other warp at the pair's barrier: it goes on, with nothing right)
-      ok = wait_warp(&sc_full[j & 3], (j >> 2) & 1) && ok;
-      ok = wait_warp(&s_full[t], j & 1) && ok;
+      if (!wait_warp(&s_full[t], j & 1)) { ok = false; break; }
       tc_fence_after();
-      uint32_t s[64];
-      tmem_ld32(t_s + 64 * half, s);
-      tmem_ld32(t_s + 64 * half + 32, s + 32);
-      const float4 sc = *reinterpret_cast<const float4*>(smem + kTlScale + (j & 3) * 32 + 16 * half);
-      const float cc = cq * sc.x;
-      const int k0 = (j0 + j) * kTlKeys + 64 * half;
-      const bool full = min_lim >= k0 + 64;                     // the warp's rows all see every key of the page
+      uint32_t s[128];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, s + 32 * q);
+      const float4 sc0 = *reinterpret_cast<const float4*>(smem + kTlScale + (j & 3) * 32);
+      const float4 sc1 = *reinterpret_cast<const float4*>(smem + kTlScale + (j & 3) * 32 + 16);
+      const float c0 = cq * sc0.x, c1 = cq * sc1.x;
+      const int k0 = (j0 + j) * kTlKeys;
+      const bool full = min_lim >= k0 + kTlKeys;                // the warp's rows all see every key of the step
       const int nv = lim - k0;
       tmem_wait_ld();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(s + 16 * q));
+      for (int q = 0; q < 8; ++q) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(s + 16 * q));
       if (!full) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
+        for (int e = 0; e < 128; ++e)
           if (e >= nv) s[e] = 0xFF800000u;                      // -inf
       }
-      float mx[4];
+      float mx[8];                                              // four chains per page
 #pragma unroll
-      for (int e = 0; e < 4; ++e) mx[e] = max3(__uint_as_float(s[e]), __uint_as_float(s[4 + e]), __uint_as_float(s[8 + e]));
-#pragma unroll
-      for (int e = 12; e < 60; e += 8) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], __uint_as_float(s[e + x]), __uint_as_float(s[e + 4 + x]));
+      for (int x = 0; x < 8; ++x) {
+        const int e = (x >> 2) * 64 + (x & 3);
+        mx[x] = max3(__uint_as_float(s[e]), __uint_as_float(s[e + 4]), __uint_as_float(s[e + 8]));
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(s[60 + x]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      float mt = top > -INFINITY ? fmaf(top, cc, sc.y) : -INFINITY;
-      float* ex = red + (j & 1) * 512 + tr;
-      ex[128 * half] = mt;
-      tc_fence_before();
-      bar_sync(pair, 64);      // both maxima are there, and both halves of S have been read
-      tc_fence_after();
-      mt = fmaxf(mt, ex[128 * (half ^ 1)]);
+      for (int e = 12; e < 60; e += 8)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int at = (x >> 2) * 64 + e + (x & 3);
+          mx[x] = max3(mx[x], __uint_as_float(s[at]), __uint_as_float(s[at + 4]));
+        }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(s[(x >> 2) * 64 + 60 + (x & 3)]));
+      const float mx0 = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]), mx1 = max3(fmaxf(mx[4], mx[5]), mx[6], mx[7]);
+      const float mt = fmaxf(mx0 > -INFINITY ? fmaf(mx0, c0, sc0.y) : -INFINITY,
+                             mx1 > -INFINITY ? fmaf(mx1, c1, sc1.y) : -INFINITY);
       const bool move = mt > m_run + kKv8Lazy;
       if (__any_sync(0xffffffffu, move)) {
         const float f = move ? ex2(m_run - mt) : 1.f;
         if (j > 0) {       // O holds steps 0 .. j - 1: their P V precede S of step j on the tensor core
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 8; ++q) {
             uint32_t ov[16];
             tmem_ld16(t_o + 16 * q, ov);
 #pragma unroll
@@ -447,26 +530,41 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
         l_run *= f;
         if (move) m_run = mt;
       }
-      const float bb = sc.y - (m_run > -INFINITY ? m_run : 0.f);
-      float lp[2] = {0.f, 0.f};
+      const float m_use = m_run > -INFINITY ? m_run : 0.f;
+      const float b0 = sc0.y - m_use, b1 = sc1.y - m_use;
+      const uint64_t cc[2] = {pack_f32(c0, c0), pack_f32(c1, c1)}, bb[2] = {pack_f32(b0, b0), pack_f32(b1, b1)};
+      uint64_t lp[4] = {0ull, 0ull, 0ull, 0ull};                 // two pairs of partial sums per page
       // (a score factor of zero, from a vanishing query, would turn a masked -inf into a NaN: masked keys get p = 0)
       auto probs = [&](auto all_seen) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          float x = ex2(fmaf(__uint_as_float(s[e]), cc, bb)), y = ex2(fmaf(__uint_as_float(s[e + 1]), cc, bb));
+        for (int e = 0; e < 128; e += 2) {
+          const int h = e >> 6;
+          float x, y;
+          unpack_f32(fma_f32x2(pack_f32(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc[h], bb[h]), x, y);
+          if ((e >> 1) % 4 == 3) {
+            ex2_poly(x, y);
+          } else {
+            x = ex2(x);
+            y = ex2(y);
+          }
           if (!decltype(all_seen)::value) {
             x = e < nv ? x : 0.f;
             y = e + 1 < nv ? y : 0.f;
           }
-          lp[0] += x;
-          lp[1] += y;
+          lp[2 * h + ((e >> 1) & 1)] = add_f32x2(lp[2 * h + ((e >> 1) & 1)], pack_f32(x, y));
           s[e >> 1] = half2_bits(x, y);
+          if (e == 62) tmem_st32(t_s, s);
         }
       };
       if (full) probs(std::true_type{});
       else probs(std::false_type{});
-      tmem_st32(t_s + 32 * half, s);
-      l_run = fmaf(lp[0] + lp[1], sc.z, l_run);
+      tmem_st32(t_s + 32, s + 32);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x, y;
+        unpack_f32(add_f32x2(lp[2 * h], lp[2 * h + 1]), x, y);
+        l_run = fmaf(x + y, h ? sc1.z : sc0.z, l_run);
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -474,13 +572,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
     }
     // output: O / L, or the split's O, m and L
     const bool have = mine > 0;
-    {
-      float* ex = red + (mine & 1) * 512 + tr;
-      ex[128 * half] = l_run;
-      bar_sync(pair, 64);
-      l_run += ex[128 * (half ^ 1)];
-    }
-    ok = (cnt == 0 || wait_warp(o_done, 0)) && ok;
+    ok = ok && (cnt == 0 || wait_warp(o_done, 0));
     tc_fence_after();
     if (ok) {
       const int qh = head * a.group + rr % a.group;
@@ -488,12 +580,12 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
       const int64_t fr = tok * a.q_heads + qh;
       const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
       const bool whole = a.nsplit == 1;
-      if (live && half == 0) {
+      if (live) {
         if (!whole) a.part_ml[fr * a.nsplit + split] = make_float2(m_run, l_run);
         else if (a.stats) a.stats[fr] = make_float2(m_run > -INFINITY ? m_run : 0.f, inv);
       }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < 4; ++q) {
         uint32_t ov[32];
         if (have) {
           tmem_ld32(t_o + 32 * q, ov);
@@ -503,9 +595,8 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
           for (int e = 0; e < 32; ++e) ov[e] = 0u;
         }
         if (!live) continue;
-        const int d = 64 * half + 32 * q;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.o + tok * a.ldo + (int64_t)qh * kKv8Dim + d);
+          uint4* dst = reinterpret_cast<uint4*>(a.o + tok * a.ldo + (int64_t)qh * kKv8Dim + 32 * q);
 #pragma unroll
           for (int e8 = 0; e8 < 4; ++e8) {
             uint32_t w[4];
@@ -518,7 +609,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
             dst[e8] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (have) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + (fr * a.nsplit + split) * kKv8Dim + d);
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + (fr * a.nsplit + split) * kKv8Dim + 32 * q);
 #pragma unroll
           for (int e4 = 0; e4 < 8; ++e4) dst[e4] = make_uint4(ov[4 * e4], ov[4 * e4 + 1], ov[4 * e4 + 2], ov[4 * e4 + 3]);
         }
@@ -527,7 +618,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -757,10 +848,11 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   const int busy = std::min(seqs, rows);             // sequences that can have queries
   p.items = (int)std::min<int64_t>(packed, packed / unit + busy);
   const int64_t blocks = (int64_t)p.items * heads;
-  const int target = 148 * 4;
   const int steps = std::max(1, (max_len + kTlKeys - 1) / kTlKeys);
-  // a split is worth its partial result when it has a few steps of its own
-  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({(target + blocks - 1) / blocks, steps / 4, 64}));
+  // A split costs its partial result and, with tiles, another setup of the block: the streaming kernel splits until
+  // the blocks fill the device four times over, the tile kernel only to fill it once.  At least four steps each.
+  const int64_t fill = p.stream ? (148 * 4 + blocks - 1) / blocks : 148 / std::max<int64_t>(blocks, 1);
+  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({fill, steps / 4, 64}));
   p.image_steps = steps;
   const int64_t images = (int64_t)seqs * steps * heads;
   p.prepare = !p.stream && p.items >= kPrepareItems * (int64_t)busy && images * 2 * kTlTile <= kPrepareBytes;
