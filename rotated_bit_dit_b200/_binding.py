@@ -385,70 +385,95 @@ def rbd_attn_int8(qc: torch.Tensor, sq: torch.Tensor, kc: torch.Tensor, sk: torc
                              _rowstride(o), _stream(stream)), "rbd_attn_int8")
 
 
-def _kv8(table: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, code_format: int) -> Kv8:
+def _at(t: torch.Tensor, cur: int) -> int:
+    """Device address of a CUDA tensor on device `cur`, the current one (see _ptr)."""
+    if t.get_device() != cur:
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        raise ValueError(f"tensor on {t.device} while cuda:{cur} is current; call under torch.cuda.device({t.device})")
+    return t.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream if not isinstance(stream, int) \
+        else stream
+
+
+def _kv8(table: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, code_format: int, cur: int) -> Kv8:
     """The rbd_kv8 of table int32 [seqs, pages per sequence], codes uint8 [pages, heads, 2, 64, 128] and
     scales float32 [pages, heads, 2]."""
-    if codes.dtype != torch.uint8 or codes.dim() != 5 or tuple(codes.shape[2:]) != (2, 64, 128) or \
-            not codes.is_contiguous():
+    s = codes.shape
+    if codes.dtype != torch.uint8 or len(s) != 5 or s[2] != 2 or s[3] != 64 or s[4] != 128 or not codes.is_contiguous():
         raise ValueError("codes must be contiguous uint8 [pages, heads, 2, 64, 128]")
-    if scales.dtype != torch.float32 or tuple(scales.shape) != (codes.shape[0], codes.shape[1], 2) or \
+    z = scales.shape
+    if scales.dtype != torch.float32 or len(z) != 3 or z[0] != s[0] or z[1] != s[1] or z[2] != 2 or \
             not scales.is_contiguous():
         raise ValueError("scales must be contiguous float32 [pages, heads, 2]")
-    if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+    t = table.shape
+    if table.dtype != torch.int32 or len(t) != 2 or (t[1] > 1 and table.stride(1) != 1):
         raise ValueError("table must be row-major int32 [seqs, pages per sequence]")
-    ldt = table.stride(0) if table.shape[0] > 1 else table.shape[1]
-    return Kv8(_ptr(codes), _ptr(scales), _ptr(table), ldt, codes.shape[0], table.shape[1], table.shape[0],
-               codes.shape[1], code_format)
+    return Kv8(_at(codes, cur), _at(scales, cur), _at(table, cur), table.stride(0) if t[0] > 1 else t[1], s[0], t[1], t[0],
+               s[1], code_format)
 
 
-def _i32(t: torch.Tensor, shape, what: str):
-    """Device address of a contiguous int32 tensor of the given shape."""
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
-    return _ptr(t)
+def _i32(t: torch.Tensor, count: int, what: str, cur: int) -> int:
+    """Device address of a contiguous int32 vector of `count` elements."""
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != count or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 [{count}]")
+    return _at(t, cur)
 
 
 def _bf16_rows(t: torch.Tensor, cols: int, what: str) -> int:
     """Row stride of bf16 [rows, >= cols]."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] < cols:
-        raise ValueError(f"{what} must be bf16 [rows, >= {cols}]")
-    return _rowstride(t) if t.shape[0] > 1 else max(t.stride(0), cols)
+    s = t.shape
+    if t.dtype != torch.bfloat16 or len(s) != 2 or s[1] < cols or t.stride(1) != 1:
+        raise ValueError(f"{what} must be bf16 [rows, >= {cols}], rows contiguous")
+    return t.stride(0) if s[0] > 1 else max(t.stride(0), cols + -cols % 8)
 
 
 def _weights(t: torch.Tensor, seqs: int, heads: int, what: str):
     """(sequence stride, head stride, columns) of float32 [seqs, heads, columns]."""
-    if t.dtype != torch.float32 or t.dim() != 3 or t.shape[0] != seqs or t.shape[1] != heads or \
-            (t.shape[2] > 1 and t.stride(2) != 1):
+    s = t.shape
+    if t.dtype != torch.float32 or len(s) != 3 or s[0] != seqs or s[1] != heads or (s[2] > 1 and t.stride(2) != 1):
         raise ValueError(f"{what} must be float32 [{seqs}, {heads}, columns] with adjacent columns")
-    return t.stride(0), (t.stride(1) if heads > 1 else max(t.stride(1), t.shape[2])), t.shape[2]
+    return t.stride(0), (t.stride(1) if heads > 1 else max(t.stride(1), s[2])), s[2]
+
+
+def _kv8_append(c: Kv8, cur: int, lens: int, cu: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    cols = c.heads * 128
+    ldk, ldv = _bf16_rows(k, cols, "k"), _bf16_rows(v, cols, "v")
+    rows = k.shape[0]
+    if rows != v.shape[0]:
+        raise ValueError("k and v differ in rows")
+    _ok(load().rbd_kv8_append(c, lens, cu, _at(k, cur), ldk, _at(v, cur), ldv, rows, _raw_stream(stream)),
+        "rbd_kv8_append")
 
 
 def rbd_kv8_append(k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
                    codes: torch.Tensor, scales: torch.Tensor, code_format: int = CODES_INT8, stream=None) -> None:
     """k, v bf16 [rows, >= heads*128] -> tokens lens[b] .. of every sequence b, whose rows are cu[b] ..
     cu[b+1] - 1 (cu int32 [seqs + 1], lens int32 [seqs]; lens is not changed)."""
-    c = _kv8(table, codes, scales, code_format)
+    cur = torch.cuda.current_device()
+    c = _kv8(table, codes, scales, code_format, cur)
+    _kv8_append(c, cur, _i32(lens, c.seqs, "lens", cur), _i32(cu, c.seqs + 1, "cu", cur), k, v, stream)
+
+
+def _kv8_read(c: Kv8, cur: int, lens: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     cols = c.heads * 128
-    ldk, ldv = _bf16_rows(k, cols, "k"), _bf16_rows(v, cols, "v")
-    if k.shape[0] != v.shape[0]:
-        raise ValueError("k and v differ in rows")
-    _ok(load().rbd_kv8_append(ctypes.byref(c), _i32(lens, (c.seqs,), "lens"), _i32(cu, (c.seqs + 1,), "cu"), _ptr(k),
-                              ldk, _ptr(v), ldv, k.shape[0], _stream(stream)), "rbd_kv8_append")
+    s = k.shape
+    if s != v.shape or len(s) != 3 or s[0] != c.seqs or s[2] != cols or k.dtype != torch.bfloat16 or \
+            v.dtype != torch.bfloat16 or not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("k and v must be contiguous bf16 [seqs, tokens, heads*128]")
+    _ok(load().rbd_kv8_read(c, lens, s[1], _at(k, cur), cols, _at(v, cur), cols, _raw_stream(stream)), "rbd_kv8_read")
 
 
 def rbd_kv8_read(lens: torch.Tensor, table: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, k: torch.Tensor,
                  v: torch.Tensor, code_format: int = CODES_INT8, stream=None) -> None:
     """The last T tokens of every sequence -> k, v bf16 [seqs, T, heads*128] (contiguous; zeros in front of a
     sequence's first token)."""
-    c = _kv8(table, codes, scales, code_format)
-    for t in (k, v):
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != c.seqs or t.shape[2] != c.heads * 128 or \
-                not t.is_contiguous():
-            raise ValueError("k and v must be contiguous bf16 [seqs, tokens, heads*128]")
-    if k.shape != v.shape:
-        raise ValueError("k and v differ in shape")
-    _ok(load().rbd_kv8_read(ctypes.byref(c), _i32(lens, (c.seqs,), "lens"), k.shape[1], _ptr(k), c.heads * 128, _ptr(v),
-                            c.heads * 128, _stream(stream)), "rbd_kv8_read")
+    cur = torch.cuda.current_device()
+    c = _kv8(table, codes, scales, code_format, cur)
+    _kv8_read(c, cur, _i32(lens, c.seqs, "lens", cur), k, v, stream)
 
 
 def rbd_kv8_attn_workspace_bytes(seqs: int, heads: int, q_heads: int, rows: int, max_len: int,
@@ -457,28 +482,40 @@ def rbd_kv8_attn_workspace_bytes(seqs: int, heads: int, q_heads: int, rows: int,
     return int(load().rbd_kv8_attn_workspace_bytes(seqs, heads, q_heads, rows, max_len, int(weigh)))
 
 
+def _kv8_attn(c: Kv8, cur: int, lens: int, cu: int, q: torch.Tensor, o: torch.Tensor, q_heads: int,
+              work: Optional[torch.Tensor], max_len: int, causal: bool, softmax_scale: float,
+              weights_in: Optional[torch.Tensor], weights_out: Optional[torch.Tensor], stream=None) -> None:
+    ldq, ldo = _bf16_rows(q, q_heads * 128, "q"), _bf16_rows(o, q_heads * 128, "o")
+    rows = q.shape[0]
+    if rows != o.shape[0]:
+        raise ValueError("q and o differ in rows")
+    w_in = w_out = None
+    w_seq = w_head = 0
+    if weights_in is not None or weights_out is not None:
+        if weights_in is None or weights_out is None:
+            raise ValueError("weights_in and weights_out go together")
+        w_seq, w_head, width = _weights(weights_out, c.seqs, c.heads, "weights_out")
+        if (weights_in is not weights_out and
+                _weights(weights_in, c.seqs, c.heads, "weights_in") != (w_seq, w_head, width)) or width < max_len:
+            raise ValueError("weights_in and weights_out must agree in shape and strides and hold max_len columns")
+        w_in, w_out = _at(weights_in, cur), _at(weights_out, cur)
+    _ok(load().rbd_kv8_attn(c, lens, cu, _at(q, cur), ldq, rows, q_heads, causal, softmax_scale, max_len, _at(o, cur), ldo,
+                            w_in, w_out, w_seq, w_head, None if work is None else _at(work, cur),
+                            0 if work is None else work.numel() * work.element_size(), _raw_stream(stream)),
+        "rbd_kv8_attn")
+
+
 def rbd_kv8_attn(q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, codes: torch.Tensor,
                  scales: torch.Tensor, o: torch.Tensor, q_heads: int, work: Optional[torch.Tensor], max_len: int,
                  causal: bool = True, softmax_scale: float = 128 ** -0.5, weights_in: Optional[torch.Tensor] = None,
                  weights_out: Optional[torch.Tensor] = None, code_format: int = CODES_INT8, stream=None) -> None:
     """q bf16 [rows, >= q_heads*128] -> o bf16, attention over the cached tokens; weights_in / weights_out
-    float32 [seqs, heads, >= max_len] add up every key's attention weight (both or neither; the same one works)."""
-    c = _kv8(table, codes, scales, code_format)
-    ldq, ldo = _bf16_rows(q, q_heads * 128, "q"), _bf16_rows(o, q_heads * 128, "o")
-    if q.shape[0] != o.shape[0]:
-        raise ValueError("q and o differ in rows")
-    w_seq = w_head = 0
-    if (weights_in is None) != (weights_out is None):
-        raise ValueError("weights_in and weights_out go together")
-    if weights_out is not None:
-        w_seq, w_head, width = _weights(weights_out, c.seqs, c.heads, "weights_out")
-        if _weights(weights_in, c.seqs, c.heads, "weights_in") != (w_seq, w_head, width) or width < max_len:
-            raise ValueError("weights_in and weights_out must agree in shape and strides and hold max_len columns")
-    _ok(load().rbd_kv8_attn(ctypes.byref(c), _i32(lens, (c.seqs,), "lens"), _i32(cu, (c.seqs + 1,), "cu"), _ptr(q), ldq,
-                            q.shape[0], q_heads, int(causal), softmax_scale, max_len, _ptr(o), ldo, _ptr(weights_in),
-                            _ptr(weights_out), w_seq, w_head, _ptr(work),
-                            0 if work is None else work.numel() * work.element_size(), _stream(stream)),
-        "rbd_kv8_attn")
+    float32 [seqs, heads, >= max_len] add up every key's attention weight (both or neither; the same one works).
+    work: rbd_kv8_attn_workspace_bytes bytes of scratch (None for 0)."""
+    cur = torch.cuda.current_device()
+    c = _kv8(table, codes, scales, code_format, cur)
+    _kv8_attn(c, cur, _i32(lens, c.seqs, "lens", cur), _i32(cu, c.seqs + 1, "cu", cur), q, o, q_heads, work, max_len,
+              causal, softmax_scale, weights_in, weights_out, stream)
 
 
 def rbd_kv8_evict(weights: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, codes: torch.Tensor,
@@ -489,17 +526,22 @@ def rbd_kv8_evict(weights: torch.Tensor, lens: torch.Tensor, table: torch.Tensor
     (weights float32 [seqs, heads, width >= lens]), quantised into the pages of dst_table int32 [seqs, >= ceil(keep / 64)]
     (none of them held by a sequence).  kept int32 [seqs, heads, keep] gets the positions (-1 behind them),
     weights_out float32 [seqs, heads, >= keep] their weights (zeros behind; may be weights), lens_out the new lengths."""
-    c = _kv8(table, codes, scales, code_format)
+    cur = torch.cuda.current_device()
+    c = _kv8(table, codes, scales, code_format, cur)
     w_seq, w_head, width = _weights(weights, c.seqs, c.heads, "weights")
     o_seq, o_head, width_out = _weights(weights_out, c.seqs, c.heads, "weights_out")
-    if dst_table.dtype != torch.int32 or dst_table.dim() != 2 or dst_table.shape[0] != c.seqs or \
-            dst_table.shape[1] * 64 < keep or (dst_table.shape[1] > 1 and dst_table.stride(1) != 1):
+    d = dst_table.shape
+    if dst_table.dtype != torch.int32 or len(d) != 2 or d[0] != c.seqs or d[1] * 64 < keep or \
+            (d[1] > 1 and dst_table.stride(1) != 1):
         raise ValueError("dst_table must be row-major int32 [seqs, >= ceil(keep / 64)]")
-    ld_dst = dst_table.stride(0) if c.seqs > 1 else dst_table.shape[1]
-    _ok(load().rbd_kv8_evict(ctypes.byref(c), _i32(lens, (c.seqs,), "lens"), _ptr(weights), w_seq, w_head, width, keep,
-                             recent, _ptr(dst_table), ld_dst, _i32(kept, (c.seqs, c.heads, keep), "kept"),
-                             _ptr(weights_out), o_seq, o_head, width_out, _i32(lens_out, (c.seqs,), "lens_out"),
-                             _stream(stream)), "rbd_kv8_evict")
+    s = kept.shape
+    if kept.dtype != torch.int32 or len(s) != 3 or s[0] != c.seqs or s[1] != c.heads or s[2] != keep or \
+            not kept.is_contiguous():
+        raise ValueError("kept must be contiguous int32 [seqs, heads, keep]")
+    _ok(load().rbd_kv8_evict(c, _i32(lens, c.seqs, "lens", cur), _at(weights, cur), w_seq, w_head, width, keep, recent,
+                             _at(dst_table, cur), dst_table.stride(0) if d[0] > 1 else d[1], _at(kept, cur),
+                             _at(weights_out, cur), o_seq, o_head, width_out, _i32(lens_out, c.seqs, "lens_out", cur),
+                             _raw_stream(stream)), "rbd_kv8_evict")
 
 
 def rbd_svdquant_fit(w: torch.Tensor, rank: int, omegas, bits: int = 4, rot_group: int = 256, scale_group: int = 0,

@@ -123,11 +123,6 @@ __device__ __forceinline__ float kv8_decode1(uint32_t w, int j) {
 // Four code bytes -> two fp16 pairs.  INT8: (b0, b2) and (b1, b3); the byte with its sign bit flipped, under the
 // exponent of 1024, is 1024 + 128 + b, from which one subtraction leaves b exactly.  E4M3: (b0, b1) and (b2, b3),
 // every E4M3 value being an fp16 value.
-__device__ __forceinline__ uint32_t hsub2_u(uint32_t a, uint32_t b) {
-  __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t m, uint32_t x) { return (a & m) ^ x; }
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t d;
   asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(two));
@@ -136,8 +131,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
 template <int FMT>
 __device__ __forceinline__ void kv8_to_f16(uint32_t w, uint32_t& p0, uint32_t& p1) {
   if (FMT == RBD_CODES_INT8) {
-    p0 = hsub2_u(and_xor(w, 0x00FF00FFu, 0x64806480u), 0x64806480u);
-    p1 = hsub2_u(and_xor(w >> 8, 0x00FF00FFu, 0x64806480u), 0x64806480u);
+    // (and, then xor: function 0x6A of one logic instruction; left to the compiler it came out as two, and the
+    // streaming kernel's integer pipe did 40% more)
+    asm("{\n\t.reg .b32 a, b, c;\n\tmov.b32 c, 0x64806480;\n\t"
+        "lop3.b32 a, %2, 0x00FF00FF, c, 0x6A;\n\tshr.u32 b, %2, 8;\n\tlop3.b32 b, b, 0x00FF00FF, c, 0x6A;\n\t"
+        "sub.f16x2 %0, a, c;\n\tsub.f16x2 %1, b, c;\n\t}"
+        : "=r"(p0), "=r"(p1)
+        : "r"(w));
   } else {
     p0 = e4m3x2_to_f16x2(w & 0xFFFFu);
     p1 = e4m3x2_to_f16x2(w >> 16);

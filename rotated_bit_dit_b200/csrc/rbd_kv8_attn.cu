@@ -48,7 +48,7 @@ struct Kv8AttnArgs {
   float* logits;       // [rows * q_heads][logit_ld]: base-2 scores (stream kernel), or null
   int64_t logit_ld;
   uint8_t* q_image;    // [heads][items][2][32 KB]: the fp16 query tiles (tile kernel), or null
-  float* q_coef;       // [heads][items][2][128]: base-2 score factor of every row of them
+  float* q_rows;       // [heads][items][2][3][128]: score factor, softmax constant and keys seen of every row of them
   uint8_t* kv_image;   // [seqs][image_steps][heads][2][32 KB]: fp16 operands of every 128-key step, or null
   float4* kv_scale;    // [seqs][image_steps][heads][2]: their page scales (s_k, log2 s_v, 1 / s_v, -)
   int image_steps;
@@ -90,50 +90,74 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-}
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
-}
-
 }  // namespace
 
 // ---------------------------------------------------------------------------
 // Few rows: warps stream pages
 // ---------------------------------------------------------------------------
-// A block takes 16 rows of one (sequence, key/value head) and one split of its
-// pages; its warps take pages in turn, each with its own ring of bulk copies (16
-// KB, keys and values of a page), its own running maximum and its own O, and are
-// joined through shared memory at the end: no warp waits for another in the loop.
-// Products on mma.sync m16n8k16 (a 128-row tcgen05 tile would be 1/8 full at
-// best), fragments straight from the bulk-copied bytes:
-//   scores   lane (g, l) of the quad layout holds channels 32 l .. 32 l + 31 of key
-//            g of every 8: the contraction order of channels is free, the query
-//            fragments use the same one;
-//   output   lane (g, l) holds channels 16 g .. 16 g + 15 of keys 2 l, 2 l + 1, 2 l
-//            + 8, 2 l + 9 of every 16: output column g of product j is channel 16 g + j.
-constexpr int kStWarps = 6;
-constexpr int kStStages = 2;
-constexpr int kStThreads = 32 * kStWarps;
-constexpr int kStRows = 16;
-constexpr uint32_t kStPage = 2 * kKv8Side;                          // 16 KB
-constexpr uint32_t kStRing = kStWarps * kStStages * kStPage;
-constexpr uint32_t kStSmem = kStRing + 256 + 2 * kStWarps * kStRows * 4 + 2 * kStRows * 4 + 128;
-constexpr int kStORow = kKv8Dim + 4;                                // padded row of a warp's O in shared memory
+// A block takes 8 NQ rows of one (sequence, key/value head) and a run of its pages.
+// Its warps take pages in turn, each with a buffer for a page's keys and one for its
+// values (8 KB bulk copies, the next page's keys on their way as soon as the scores
+// are formed), its own running maximum and its own O, and are joined through shared
+// memory at the end: no warp waits for another in the loop.  The products are
+// mma.sync m16n8k16 with keys (then channels) as the 16 and queries as the 8: a
+// single token of a grouped head fills an 8 half or whole, where a 128-row tcgen05
+// tile would be 1/32 full.  Fragments come straight from the bulk-copied bytes, since
+// the order of a contraction is free:
+//   scores^T = K Q^T   lane (g, l) holds channels 32 l .. 32 l + 31 of keys g and g + 8
+//                      of every 16; the query fragments use the same order;
+//   out^T = V^T P^T    lane (g, l) holds channels 16 g .. 16 g + 15 of keys 2 l, 2 l + 1,
+//                      2 l + 8, 2 l + 9 of every 16: row g of product j is channel
+//                      16 g + 2 j, row g + 8 the next; P^T is the transposed scores'
+//                      fragment (one 8 x 8 transpose for 8 keys).
+// What bounds it is reading the cache once; close behind come the instructions that
+// convert codes (about 800 of a page's 1000 a warp), so what else a page needs (its
+// index, the logarithm and inverse of its scale) is worked out 32 pages at a time, one
+// a lane.
+constexpr uint32_t kStPage = 2 * kKv8Side;                           // 16 KB: a warp's two buffers
+constexpr int kStORow = kKv8Dim + 4;                                 // padded row of a warp's O in shared memory
 
-template <int FMT>
-__global__ void __launch_bounds__(kStThreads, 1) kv8_stream_kernel(const Kv8View c, const Kv8AttnArgs a) {
+template <int NQ>
+struct StreamShape {
+  static constexpr int kWarps = 12;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kRows = 8 * NQ;
+  static constexpr uint32_t kRing = kWarps * kStPage;
+  static constexpr uint32_t kSmem = kRing + 256 + (2 * kWarps * kRows + 2 * kRows) * 4 + 128;
+  static_assert(kStPage >= kRows * kStORow * 4, "a warp's O fits its buffers");
+};
+
+// Transposes the 8 x 8 matrix of 16-bit values whose row g the lanes 4 g .. 4 g + 3 hold in pairs.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Maximum and sum over the lanes that share l (the 8 values of g).
+__device__ __forceinline__ float col_max(float x) {
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+  return x;
+}
+__device__ __forceinline__ float col_sum(float x) {
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
+
+template <int FMT, int NQ>
+__global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kernel(const Kv8View c, const Kv8AttnArgs a) {
+  using Sh = StreamShape<NQ>;
+  constexpr int W = Sh::kWarps, ROWS = Sh::kRows;
   extern __shared__ unsigned char smem_dyn[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 127u) & ~uintptr_t(127u));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStRing);
-  float* red_m = reinterpret_cast<float*>(smem + kStRing + 256);   // [warps][16]
-  float* red_l = red_m + kStWarps * kStRows;                        // [warps][16]
-  float* row_l = red_l + kStWarps * kStRows;                        // [16]
-  float* row_m = row_l + kStRows;                                   // [16]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kRing);
+  float* red_m = reinterpret_cast<float*>(smem + Sh::kRing + 256);   // [warps][rows]
+  float* red_l = red_m + W * ROWS;                                   // [warps][rows]
+  float* row_l = red_l + W * ROWS;                                   // [rows]
+  float* row_m = row_l + ROWS;                                       // [rows]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, l = lane & 3;
   const int head = blockIdx.y, split = blockIdx.z;
@@ -141,55 +165,70 @@ __global__ void __launch_bounds__(kStThreads, 1) kv8_stream_kernel(const Kv8View
   auto tiles_of = [&](int b) {
     int r0, n;
     kv8_rows(a.cu, b, a.rows, r0, n);
-    return (int)(((int64_t)n * a.group + kStRows - 1) / kStRows);
+    return (int)(((int64_t)n * a.group + ROWS - 1) / ROWS);
   };
   int b, tile;
   if (!kv8_find(c.seqs, blockIdx.x, tiles_of, b, tile)) return;
   int r0, n;
   kv8_rows(a.cu, b, a.rows, r0, n);
   const int len = kv8_len(c, a, b);
-  const int row_first = tile * kStRows;
-  const int nrows = min(kStRows, n * a.group - row_first);
+  const int row_first = tile * ROWS;
+  const int nrows = min(ROWS, n * a.group - row_first);
   const int vis = min(len, kv8_visible(a.causal, len, n, (row_first + nrows - 1) / a.group));
-  const int npages = (vis + kKv8Page - 1) / kKv8Page;
-  const int per = (npages + a.nsplit - 1) / a.nsplit;
-  const int p0 = split * per, p1 = min(npages, p0 + per);
-  const int cnt = p1 - p0 > warp ? (p1 - p0 - warp + kStWarps - 1) / kStWarps : 0;
+  // this split's run of pages: the same number for every sequence, so that blocks take equally long
+  const int per = ((a.max_len + kKv8Page - 1) / kKv8Page + a.nsplit - 1) / a.nsplit;
+  const int p0 = min(split * per, (vis + kKv8Page - 1) / kKv8Page);
+  const int p1 = min(p0 + per, (vis + kKv8Page - 1) / kKv8Page);
+  const int cnt = p1 - p0 > warp ? (p1 - p0 - warp + W - 1) / W : 0;
 
+  uint64_t* full = bars + 2 * warp;                                  // keys, values
   if (lane == 0) {
-    for (int s = 0; s < kStStages; ++s) mbar_init(&bars[warp * kStStages + s], 1);
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
     fence_barrier_init();
   }
   __syncwarp();
-  unsigned char* ring = smem + warp * kStStages * kStPage;
-  uint64_t* full = bars + warp * kStStages;
-  auto page_at = [&](int i) { return i < cnt ? kv8_page(c, b, p0 + warp + i * kStWarps) : -1; };
-  auto issue = [&](int i, int page) {
-    if (i >= cnt || lane != 0) return;
-    uint64_t* bar = &full[i % kStStages];
-    if (page >= 0) {
-      mbar_arrive_expect_tx(bar, kStPage);
-      bulk_load(ring + (i % kStStages) * kStPage, c.codes + kv8_tile(c, page, head, 0), kStPage, bar);
-    } else {
-      mbar_arrive(bar);
+  unsigned char* ring = smem + warp * kStPage;
+  // 32 of the warp's pages at a time: lane i knows page i, its scales, log2 s_v and 1 / s_v
+  int my_page = -1;
+  float my_sk = 1.f, my_lsv = 0.f, my_inv = 1.f;
+  auto look_up = [&](int i0) {
+    my_page = -1;
+    if (i0 + lane < cnt) {
+      my_page = kv8_page(c, b, p0 + warp + (i0 + lane) * W);
+      if (my_page >= 0) {
+        const float2 sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, my_page, head, 0));
+        my_sk = sc.x;
+        my_lsv = log2f(sc.y);
+        my_inv = 1.0f / sc.y;
+      }
     }
   };
-  int pages[kStStages + 1];
-#pragma unroll
-  for (int i = 0; i <= kStStages; ++i) pages[i] = page_at(i);
-#pragma unroll
-  for (int i = 0; i < kStStages; ++i) issue(i, pages[i]);
+  auto issue = [&](int side, int page) {       // an index outside the pool: the buffer's old contents, skipped below
+    if (lane != 0) return;
+    if (page >= 0) {
+      mbar_arrive_expect_tx(&full[side], kKv8Side);
+      bulk_load(ring + side * kKv8Side, c.codes + kv8_tile(c, page, head, side), kKv8Side, &full[side]);
+    } else {
+      mbar_arrive(&full[side]);
+    }
+  };
+  look_up(0);
+  int page = __shfl_sync(0xffffffffu, my_page, 0);
+  if (cnt > 0) {
+    issue(0, page);
+    issue(1, page);
+  }
 
-  // query fragments: row g and row g + 8, channels 32 l .. 32 l + 31
-  uint32_t qa[8][4];
-  float coef[2];
-  int lim[2];
+  // query fragments: row g of every 8, channels 32 l .. 32 l + 31
+  uint32_t qb[NQ][8][2];
+  float coef[NQ][2];                                   // of rows 2 l and 2 l + 1 of every 8
+  int lim[NQ][2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = row_first + g + 8 * h;
-    const bool live = g + 8 * h < nrows;
+  for (int q = 0; q < NQ; ++q) {
+    const int r = row_first + 8 * q + g;
     uint4 w[4];
-    if (live) {
+    if (8 * q + g < nrows) {
       const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(r0 + r / a.group) * a.ldq +
                                                         (int64_t)(head * a.group + r % a.group) * kKv8Dim + 32 * l);
 #pragma unroll
@@ -209,8 +248,12 @@ __global__ void __launch_bounds__(kStThreads, 1) kv8_stream_kernel(const Kv8View
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     float f, inv;
     kv8_row_scale(amax, f, inv);
-    coef[h] = inv * a.scale_log2;
-    lim[h] = live ? kv8_visible(a.causal, len, n, r / a.group) : vis;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int rr = 8 * q + 2 * l + x;
+      coef[q][x] = __shfl_sync(0xffffffffu, inv, 4 * (2 * l + x)) * a.scale_log2;
+      lim[q][x] = rr < nrows ? kv8_visible(a.causal, len, n, (row_first + rr) / a.group) : vis;
+    }
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
       const uint4 u = w[kk >> 1];
@@ -218,201 +261,223 @@ __global__ void __launch_bounds__(kStThreads, 1) kv8_stream_kernel(const Kv8View
       const float d0 = __uint_as_float(w0 << 16) * f, d1 = __uint_as_float(w0 & 0xFFFF0000u) * f;
       const float d2 = __uint_as_float(w1 << 16) * f, d3 = __uint_as_float(w1 & 0xFFFF0000u) * f;
       // the pairs kv8_to_f16 makes of a word's four codes
-      qa[kk][h] = FMT == RBD_CODES_INT8 ? half2_bits(d0, d2) : half2_bits(d0, d1);
-      qa[kk][2 + h] = FMT == RBD_CODES_INT8 ? half2_bits(d1, d3) : half2_bits(d2, d3);
+      qb[q][kk][0] = FMT == RBD_CODES_INT8 ? half2_bits(d0, d2) : half2_bits(d0, d1);
+      qb[q][kk][1] = FMT == RBD_CODES_INT8 ? half2_bits(d1, d3) : half2_bits(d2, d3);
     }
   }
-  const int min_lim = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
+  int min_lim = lim[0][0];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) min_lim = min(min_lim, min(lim[q][0], lim[q][1]));
+  min_lim = __reduce_min_sync(0xffffffffu, min_lim);
 
-  float o[16][4];
+  float o[NQ][8][4];
+  float m_run[NQ][2], l_run[NQ][2];
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
+  for (int q = 0; q < NQ; ++q) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-  auto scales_of = [&](int page) {
-    return page >= 0 ? *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page, head, 0)) : make_float2(1.f, 1.f);
-  };
-  float2 sc_next = scales_of(pages[0]);
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[q][j][e] = 0.f;
+    m_run[q][0] = m_run[q][1] = -INFINITY;
+    l_run[q][0] = l_run[q][1] = 0.f;
+  }
   bool ok = true;
   for (int i = 0; i < cnt; ++i) {
-    const float2 sc = sc_next;
-    const int page = pages[0];
-    sc_next = scales_of(pages[1]);
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[i % kStStages], (i / kStStages) & 1))) { ok = false; break; }
-    if (page >= 0) {
-      const unsigned char* kt = ring + (i % kStStages) * kStPage;
-      const unsigned char* vt = kt + kKv8Side;
-      const int t0 = (p0 + warp + i * kStWarps) * kKv8Page;
-      float s[8][4];
+    const float sk = __shfl_sync(0xffffffffu, my_sk, i & 31), lsv = __shfl_sync(0xffffffffu, my_lsv, i & 31);
+    const float inv_sv = __shfl_sync(0xffffffffu, my_inv, i & 31);
+    if (((i + 1) & 31) == 0) look_up(i + 1);
+    const int next = __shfl_sync(0xffffffffu, my_page, (i + 1) & 31);
+    const bool more = i + 1 < cnt;
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[0], i & 1))) { ok = false; break; }
+    // a page outside the pool: no query sees its tokens
+    const int t0 = page >= 0 ? (p0 + warp + i * W) * kKv8Page : 1 << 30;
+    const bool masked = t0 + kKv8Page > min_lim;
+    float s[NQ][4][4];                                 // token 16 mt + g (+ 8), rows 2 l, 2 l + 1
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-        const int t = 8 * nt + g;
-        const uint4 u0 = *reinterpret_cast<const uint4*>(kt + kv8_chunk(t, 2 * l));
-        const uint4 u1 = *reinterpret_cast<const uint4*>(kt + kv8_chunk(t, 2 * l + 1));
-        const uint32_t ws[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+    for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          uint32_t b0, b1;
-          kv8_to_f16<FMT>(ws[kk], b0, b1);
-          mma_f16(s[nt], qa[kk], b0, b1);
-        }
+      for (int q = 0; q < NQ; ++q) s[q][mt][0] = s[q][mt][1] = s[q][mt][2] = s[q][mt][3] = 0.f;
+      uint4 u[2][2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        u[x][0] = *reinterpret_cast<const uint4*>(ring + kv8_chunk(16 * mt + 8 * x + g, 2 * l));
+        u[x][1] = *reinterpret_cast<const uint4*>(ring + kv8_chunk(16 * mt + 8 * x + g, 2 * l + 1));
       }
-      const bool masked = t0 + kKv8Page > min_lim;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        uint32_t af[4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint4& v = u[x][kk >> 2];
+          const uint32_t w = (kk & 3) == 0 ? v.x : (kk & 3) == 1 ? v.y : (kk & 3) == 2 ? v.z : v.w;
+          kv8_to_f16<FMT>(w, af[x], af[2 + x]);
+        }
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) mma_f16(s[q][mt], af, qb[q][kk][0], qb[q][kk][1]);
+      }
+    }
+    __syncwarp();
+    fence_async_shared();
+    if (more) issue(0, next);                          // the keys' buffer has been read
+    float ck[NQ][2];
+    uint32_t pb[NQ][4][2];                             // P^T fragments of 16 keys
+    float mt_[NQ][2];
+    bool move = false;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
       if (masked) {
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
+        for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (t0 + 8 * nt + 2 * l + (e & 1) >= lim[e >> 1]) s[nt][e] = -INFINITY;
+            if (t0 + 16 * mt + g + 8 * (e >> 1) >= lim[q][e & 1]) s[q][mt][e] = -INFINITY;
       }
-      const float lsv = log2f(sc.y), inv_sv = 1.0f / sc.y;
-      float base[2], ck[2];
-      bool move = false;
-      float mt[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float mx = -INFINITY;
+      for (int x = 0; x < 2; ++x) {
+        float mx = fmaxf(s[q][0][x], s[q][0][2 + x]);
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * h], s[nt][2 * h + 1]));
-        mx = quad_max(mx);
-        ck[h] = coef[h] * sc.x;
-        mt[h] = mx > -INFINITY ? fmaf(mx, ck[h], lsv) : -INFINITY;
-        move = move || mt[h] > m_run[h] + kKv8Lazy;
+        for (int mt = 1; mt < 4; ++mt) mx = fmaxf(mx, fmaxf(s[q][mt][x], s[q][mt][2 + x]));
+        mx = col_max(mx);
+        ck[q][x] = coef[q][x] * sk;
+        mt_[q][x] = mx > -INFINITY ? fmaf(mx, ck[q][x], lsv) : -INFINITY;
+        move = move || mt_[q][x] > m_run[q][x] + kKv8Lazy;
       }
-      if (__any_sync(0xffffffffu, move)) {
+    }
+    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
         float f[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool up = mt[h] > m_run[h] + kKv8Lazy;
-          f[h] = up ? ex2(m_run[h] - mt[h]) : 1.f;
-          if (up) m_run[h] = mt[h];
-          l_run[h] *= f[h];
+        for (int x = 0; x < 2; ++x) {
+          const bool up = mt_[q][x] > m_run[q][x] + kKv8Lazy;
+          f[x] = up ? ex2(m_run[q][x] - mt_[q][x]) : 1.f;
+          if (up) m_run[q][x] = mt_[q][x];
+          l_run[q][x] *= f[x];
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          o[j][0] *= f[0];
-          o[j][1] *= f[0];
-          o[j][2] *= f[1];
-          o[j][3] *= f[1];
-        }
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[q][j][e] *= f[e & 1];
       }
+    }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) base[h] = lsv - (m_run[h] > -INFINITY ? m_run[h] : 0.f);
-      if (a.logits) {
+    for (int q = 0; q < NQ; ++q) {
+      if (a.logits && page >= 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = row_first + g + 8 * h;
-          if (g + 8 * h < nrows) {
+        for (int x = 0; x < 2; ++x) {
+          const int rr = 8 * q + 2 * l + x;
+          if (rr < nrows) {
+            const int r = row_first + rr;
             float* dst = a.logits + ((int64_t)(r0 + r / a.group) * a.q_heads + head * a.group + r % a.group) * a.logit_ld +
-                         t0 + 2 * l;
+                         t0 + g;
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-              *reinterpret_cast<float2*>(dst + 8 * nt) = make_float2(s[nt][2 * h] * ck[h], s[nt][2 * h + 1] * ck[h]);
+            for (int e = 0; e < 8; ++e) dst[8 * e] = s[q][e >> 1][2 * (e & 1) + x] * ck[q][x];
           }
         }
       }
-      float lp[2] = {0.f, 0.f};
+      float base[2], lp[2] = {0.f, 0.f};
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
+      for (int x = 0; x < 2; ++x) base[x] = lsv - (m_run[q][x] > -INFINITY ? m_run[q][x] : 0.f);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float p = ex2(fmaf(s[nt][e], ck[e >> 1], base[e >> 1]));
-          if (masked && t0 + 8 * nt + 2 * l + (e & 1) >= lim[e >> 1]) p = 0.f;
-          lp[e >> 1] += p;
-          s[nt][e] = p;
+          float p = ex2(fmaf(s[q][mt][e], ck[q][e & 1], base[e & 1]));
+          // (a score factor of zero, from a vanishing query, would turn a masked -inf into a NaN)
+          if (masked && t0 + 16 * mt + g + 8 * (e >> 1) >= lim[q][e & 1]) p = 0.f;
+          lp[e & 1] += p;
+          s[q][mt][e] = p;
         }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) l_run[h] = fmaf(lp[h], inv_sv, l_run[h]);
-      const int valid = len - t0;      // rows of the page behind this hold nothing (an E4M3 NaN pattern perhaps)
+        for (int x = 0; x < 2; ++x) pb[q][mt][x] = transpose_8x8(half2_bits(s[q][mt][2 * x], s[q][mt][2 * x + 1]));
+      }
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t pa[4] = {half2_bits(s[2 * kk][0], s[2 * kk][1]), half2_bits(s[2 * kk][2], s[2 * kk][3]),
-                                half2_bits(s[2 * kk + 1][0], s[2 * kk + 1][1]),
-                                half2_bits(s[2 * kk + 1][2], s[2 * kk + 1][3])};
-        uint32_t w[4][4];
+      for (int x = 0; x < 2; ++x) l_run[q][x] = fmaf(lp[x], inv_sv, l_run[q][x]);
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[1], i & 1))) { ok = false; break; }
+    const unsigned char* vt = ring + kKv8Side;
+    const int valid = len - t0;        // rows of the page behind this hold nothing (an E4M3 NaN pattern perhaps)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int t = 16 * kk + 2 * l + (q & 1) + 8 * (q >> 1);
-          uint4 u = *reinterpret_cast<const uint4*>(vt + kv8_chunk(t, g));
-          if (FMT != RBD_CODES_INT8 && t >= valid) u = make_uint4(0u, 0u, 0u, 0u);
-          w[q][0] = u.x;
-          w[q][1] = u.y;
-          w[q][2] = u.z;
-          w[q][3] = u.w;
-        }
+    for (int mt = 0; mt < 4; ++mt) {
+      uint32_t w[4][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          // byte order in which kv8_to_f16 pairs the two keys of a channel
-          constexpr uint32_t lo = FMT == RBD_CODES_INT8 ? 0x5410u : 0x5140u;
-          constexpr uint32_t hi = FMT == RBD_CODES_INT8 ? 0x7632u : 0x7362u;
-          uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
-          kv8_to_f16<FMT>(prmt(w[0][x], w[1][x], lo), a0, a1);
-          kv8_to_f16<FMT>(prmt(w[0][x], w[1][x], hi), a2, a3);
-          kv8_to_f16<FMT>(prmt(w[2][x], w[3][x], lo), c0, c1);
-          kv8_to_f16<FMT>(prmt(w[2][x], w[3][x], hi), c2, c3);
-          mma_f16(o[4 * x], pa, a0, c0);
-          mma_f16(o[4 * x + 1], pa, a1, c1);
-          mma_f16(o[4 * x + 2], pa, a2, c2);
-          mma_f16(o[4 * x + 3], pa, a3, c3);
+      for (int x = 0; x < 4; ++x) {
+        const int t = 16 * mt + 2 * l + (x & 1) + 8 * (x >> 1);
+        uint4 u = *reinterpret_cast<const uint4*>(vt + kv8_chunk(t, g));
+        if (FMT != RBD_CODES_INT8 && masked && t >= valid) u = make_uint4(0u, 0u, 0u, 0u);
+        w[x][0] = u.x;
+        w[x][1] = u.y;
+        w[x][2] = u.z;
+        w[x][3] = u.w;
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        // byte order in which kv8_to_f16 pairs the two keys of a channel
+        constexpr uint32_t lo = FMT == RBD_CODES_INT8 ? 0x5410u : 0x5140u;
+        constexpr uint32_t hi = FMT == RBD_CODES_INT8 ? 0x7632u : 0x7362u;
+        uint32_t a0[4], a1[4];
+        kv8_to_f16<FMT>(prmt(w[0][x], w[1][x], lo), a0[0], a0[1]);
+        kv8_to_f16<FMT>(prmt(w[2][x], w[3][x], lo), a0[2], a0[3]);
+        kv8_to_f16<FMT>(prmt(w[0][x], w[1][x], hi), a1[0], a1[1]);
+        kv8_to_f16<FMT>(prmt(w[2][x], w[3][x], hi), a1[2], a1[3]);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          mma_f16(o[q][2 * x], a0, pb[q][mt][0], pb[q][mt][1]);
+          mma_f16(o[q][2 * x + 1], a1, pb[q][mt][0], pb[q][mt][1]);
         }
       }
     }
     __syncwarp();
     fence_async_shared();
-    issue(i + kStStages, pages[kStStages]);
-#pragma unroll
-    for (int q = 0; q < kStStages; ++q) pages[q] = pages[q + 1];
-    pages[kStStages] = page_at(i + kStStages + 1);
+    if (more) issue(1, next);
+    page = next;
   }
   if (!ok) {   // copies still in flight land in this block's shared memory
     const uint64_t t = globaltimer_ns();
     while (globaltimer_ns() - t < 200000ull) {}
   }
-  l_run[0] = quad_sum(l_run[0]);
-  l_run[1] = quad_sum(l_run[1]);
   // this warp's O over its own ring, every copy into which has been consumed
   float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float* dst = mine + (g + 8 * h) * kStORow + 32 * l;
+  for (int q = 0; q < NQ; ++q)
 #pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-      *reinterpret_cast<float4*>(dst + j) =
-          make_float4(o[j][2 * h], o[j + 1][2 * h], o[j + 2][2 * h], o[j + 3][2 * h]);
-      *reinterpret_cast<float4*>(dst + 16 + j) =
-          make_float4(o[j][2 * h + 1], o[j + 1][2 * h + 1], o[j + 2][2 * h + 1], o[j + 3][2 * h + 1]);
+    for (int x = 0; x < 2; ++x) {
+      const float lsum = col_sum(l_run[q][x]);
+      const int rr = 8 * q + 2 * l + x;
+      float* dst = mine + rr * kStORow + 16 * g;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2)
+        *reinterpret_cast<float4*>(dst + 2 * j) =
+            make_float4(o[q][j][x], o[q][j][2 + x], o[q][j + 1][x], o[q][j + 1][2 + x]);
+      if (g == 0) {
+        red_m[warp * ROWS + rr] = m_run[q][x];
+        red_l[warp * ROWS + rr] = lsum;
+      }
     }
-    if (l == 0) {
-      red_m[warp * kStRows + g + 8 * h] = m_run[h];
-      red_l[warp * kStRows + g + 8 * h] = l_run[h];
-    }
-  }
   __syncthreads();
-  if (tid < kStRows) {
+  if (tid < ROWS) {
     float m = -INFINITY, lsum = 0.f;
-    for (int w = 0; w < kStWarps; ++w) m = fmaxf(m, red_m[w * kStRows + tid]);
-    for (int w = 0; w < kStWarps; ++w) {
-      const float mw = red_m[w * kStRows + tid];
-      const float f = mw > -INFINITY ? ex2(mw - m) : 0.f;
+    for (int w = 0; w < W; ++w) m = fmaxf(m, red_m[w * ROWS + tid]);
+    for (int w = 0; w < W; ++w) {
+      const float mw = red_m[w * ROWS + tid];
       // a row of NaN scores has no maximum but a NaN sum
-      lsum += red_l[w * kStRows + tid] * (mw > -INFINITY ? f : 1.f);
-      red_m[w * kStRows + tid] = mw > -INFINITY ? f : 1.f;
+      const float f = mw > -INFINITY ? ex2(mw - m) : 1.f;
+      lsum += red_l[w * ROWS + tid] * f;
+      red_m[w * ROWS + tid] = f;
     }
     row_m[tid] = m;
     row_l[tid] = lsum;
   }
   __syncthreads();
-  for (int e = tid; e < kStRows * 16; e += kStThreads) {
+  for (int e = tid; e < ROWS * 16; e += Sh::kThreads) {
     const int rr = e >> 4, d = (e & 15) * 8;
     if (rr >= nrows) continue;
     float acc[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) acc[x] = 0.f;
-    for (int w = 0; w < kStWarps; ++w) {
-      const float f = red_m[w * kStRows + rr];
-      const float* src = reinterpret_cast<const float*>(smem + w * kStStages * kStPage) + rr * kStORow + d;
+    for (int w = 0; w < W; ++w) {
+      const float f = red_m[w * ROWS + rr];
+      const float* src = reinterpret_cast<const float*>(smem + w * kStPage) + rr * kStORow + d;
       const float4 u = *reinterpret_cast<const float4*>(src), v = *reinterpret_cast<const float4*>(src + 4);
       acc[0] = fmaf(u.x, f, acc[0]);
       acc[1] = fmaf(u.y, f, acc[1]);
@@ -439,9 +504,11 @@ __global__ void __launch_bounds__(kStThreads, 1) kv8_stream_kernel(const Kv8View
       *reinterpret_cast<uint4*>(a.o + tok * a.ldo + (int64_t)qh * kKv8Dim + d) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
       if (a.stats && d == 0) a.stats[fr] = make_float2(row_m[rr] > -INFINITY ? row_m[rr] : 0.f, inv);
     } else {
-      float4* dst = reinterpret_cast<float4*>(a.part_o + (fr * a.nsplit + split) * kKv8Dim + d);
-      dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (lsum != 0.f) {               // (the join reads nothing of a split without keys)
+        float4* dst = reinterpret_cast<float4*>(a.part_o + (fr * a.nsplit + split) * kKv8Dim + d);
+        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      }
       if (d == 0) a.part_ml[fr * a.nsplit + split] = make_float2(row_m[rr], lsum);
     }
   }

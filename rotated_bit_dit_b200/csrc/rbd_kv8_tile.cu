@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
         if (a.q_image && split == 0) {
           const int64_t img = ((int64_t)head * a.items + item) * 2 + qt;
           *reinterpret_cast<uint4*>(a.q_image + img * kTlTile + tile_chunk(tr, ch)) = hv;
-          if (ch == 0) a.q_coef[img * kTlRows + tr] = inv * a.scale_log2;
+          if (ch == 0) a.q_rows[img * 3 * kTlRows + tr] = inv * a.scale_log2;
         }
       }
     }
@@ -629,38 +629,78 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
 // ---------------------------------------------------------------------------
 // A block per (128 keys, key/value head, sequence) computes S^T = K Q^T for every
 // query tile that sees them, the keys on the TMEM lanes: a thread owns a key and
-// adds 2^(x - m) / L over the columns, with the rows' final m and L, in a fixed
-// order and without atomics.  The query tiles come from the images the attention
-// left behind (one 32 KB bulk copy each).
+// adds 2^(x - m) / L = 2^(x + c) over the columns, c = -(m + log2 L) from the rows'
+// final m and L, in a fixed order and without atomics.  The query tiles come from
+// the images the attention left behind (one 32 KB bulk copy each), and so do the rows'
+// factors, constants and numbers of keys, which kv8_rows_kernel completes (gathered by
+// a warp of this kernel they took 4700 cycles a tile, most of its time).  Bound by the
+// special-function unit (1024 cycles a 128 x 128 tile, Q.K^T 512); the columns'
+// factors and constants are broadcast reads, four columns at a time.  Two blocks an
+// SM, so that one sums while the other waits.  Under a causal mask the first keys see
+// every tile and the last ones one: with few blocks the tiles of each are cut into
+// `parts`, whose sums kv8_weigh_add_kernel adds in order.
 //   warps 0-3, 4-7  sums, query tiles in turn;  warp 8  producer;  warp 9  TMEM owner and MMA issuer.
 namespace {
 constexpr int kWgThreads = 320;
-constexpr int kWgStages = 3;
-constexpr uint32_t kWgQ = kTlTile;                                  // after the keys
-constexpr uint32_t kWgPar = kWgQ + kWgStages * kTlTile;             // 4 slots x 128 rows x (factor, m, 1 / L, keys seen)
-constexpr uint32_t kWgSum = kWgPar + 4 * kTlRows * 16;              // 128 floats
+constexpr uint32_t kWgQ = kTlTile;                                  // after the keys: 2 query tiles
+constexpr uint32_t kWgRowsBytes = 3 * kTlRows * 4;                  // (factor, constant, keys seen) of 128 rows
+constexpr uint32_t kWgPar = kWgQ + 2 * kTlTile;                     // 4 slots of those
+constexpr uint32_t kWgSum = kWgPar + 4 * kWgRowsBytes;              // 128 floats
 constexpr uint32_t kWgBar = kWgSum + 512;
 constexpr uint32_t kWgSmem = kWgBar + 256 + 1024;
 }  // namespace
 
+// The rows' constants c = -(m + log2 L) and numbers of keys seen, beside their factors: [heads][items][2][3][128].
+__global__ void __launch_bounds__(2 * kTlRows) kv8_rows_kernel(const Kv8View c, const Kv8AttnArgs a) {
+  auto tiles_of = [&](int b) {
+    int r0, n;
+    kv8_rows(a.cu, b, a.rows, r0, n);
+    return (int)(((int64_t)n * a.group + 2 * kTlRows - 1) / (2 * kTlRows));
+  };
+  int b, tile;
+  if (!kv8_find(c.seqs, blockIdx.x, tiles_of, b, tile)) return;
+  int r0, n;
+  kv8_rows(a.cu, b, a.rows, r0, n);
+  const int len = kv8_len(c, a, b);
+  const int head = blockIdx.y;
+  const int rr = tile * 2 * kTlRows + threadIdx.x;
+  float k = -INFINITY;                          // no such row, or one without keys: 2^(-inf) = 0
+  int seen = 0;
+  if (rr < n * a.group) {
+    const int i = rr / a.group;
+    const float2 s = a.stats[(int64_t)(r0 + i) * a.q_heads + head * a.group + (rr - i * a.group)];
+    if (s.y != 0.f) k = log2f(s.y) - s.x;
+    seen = kv8_visible(a.causal, len, n, i);
+  }
+  const int64_t img = ((int64_t)head * a.items + blockIdx.x) * 2 + (threadIdx.x >> 7);
+  float* rows = a.q_rows + img * 3 * kTlRows + (threadIdx.x & 127);
+  rows[kTlRows] = k;
+  reinterpret_cast<int*>(rows)[2 * kTlRows] = seen;
+}
+
 template <int FMT>
-__global__ void __launch_bounds__(kWgThreads, 1)
+__global__ void __launch_bounds__(kWgThreads, 2)
     kv8_weigh_tile_kernel(const Kv8View c, const Kv8AttnArgs a, const float* w_in, float* w_out, int64_t w_seq,
-                          int64_t w_head) {
+                          int64_t w_head, float* part_out, int parts) {
   extern __shared__ unsigned char smem_dyn[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023u) & ~uintptr_t(1023u));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWgBar);
-  uint64_t* q_full = bars;          // [3] bulk copy
-  uint64_t* q_empty = bars + 3;     // [3] commit
-  uint64_t* par_full = bars + 6;    // [4] producer warp
-  uint64_t* s_full = bars + 10;     // [4] commit
-  uint64_t* s_empty = bars + 14;    // [4] 4 summing warps
-  uint64_t* drain = bars + 18;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 20);
+  uint64_t* q_full = bars;          // [2] bulk copies
+  uint64_t* q_empty = bars + 2;     // [2] commit
+  uint64_t* s_full = bars + 6;      // [2] commit
+  uint64_t* s_empty = bars + 8;     // [2] 4 summing warps
+  uint64_t* drain = bars + 10;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 12);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.z, head = blockIdx.y, k0 = blockIdx.x * kTlKeys;
+  // the key block is the slowest index: under a causal mask the first ones take longest and start first
+  const int each = parts * c.heads * c.seqs;
+  const int k0 = (int)(blockIdx.x / each) * kTlKeys;
+  int rest = (int)(blockIdx.x % each);
+  const int part = rest % parts;
+  rest /= parts;
+  const int head = rest % c.heads, b = rest / c.heads;
   const int len = kv8_len(c, a, b);
   if (k0 >= len) return;
   // first item (256 query rows) of this sequence in the images: the items of the sequences in front of it
@@ -676,17 +716,16 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   kv8_rows(a.cu, b, a.rows, r0, n);
   const int total = n * a.group;
   const int i_first = a.causal ? max(0, k0 - (len - n)) : 0;          // first query token that sees key k0
-  const int tile0 = min(i_first, n) * a.group / kTlRows;
-  const int ntiles = (total + kTlRows - 1) / kTlRows;
-  const int cnt = max(0, ntiles - tile0);
+  const int seen0 = min(i_first, n) * a.group / kTlRows;
+  const int nseen = max(0, (total + kTlRows - 1) / kTlRows - seen0);
+  const int per = (nseen + parts - 1) / parts;
+  const int tile0 = seen0 + part * per;
+  const int cnt = max(0, min(per, nseen - part * per));
 
   if (tid == 0) {
-    for (int i = 0; i < kWgStages; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&par_full[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
     }
@@ -694,19 +733,28 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     fence_barrier_init();
   }
   if (warp == 9) {
-    tmem_alloc(tmem_holder, 512);
+    tmem_alloc(tmem_holder, 256);
     tmem_relinquish();
     tc_fence_before();
   }
   // the block's keys: 128 tokens x 8 chunks
-  for (int e = tid; e < kTlKeys * 8; e += kWgThreads) {
-    const int t = e >> 3, ch = e & 7;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (k0 + t < len) {
-      const int page = kv8_page(c, b, (k0 + t) / kKv8Page);
-      if (page >= 0) w = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, page, head, 0) + kv8_chunk(t & 63, ch));
+  {
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = tid + i * kWgThreads, t = e >> 3;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (e < kTlKeys * 8 && k0 + t < len) {
+        const int page = kv8_page(c, b, (k0 + t) / kKv8Page);
+        if (page >= 0)
+          w[i] = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, page, head, 0) + kv8_chunk(t & 63, e & 7));
+      }
     }
-    store_codes<FMT>(smem, t, ch, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = tid + i * kWgThreads;
+      if (e < kTlKeys * 8) store_codes<FMT>(smem, e >> 3, e & 7, w[i]);
+    }
   }
   fence_async_shared();
   __syncthreads();
@@ -714,59 +762,45 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   const uint32_t tmem = *tmem_holder;
 
   if (warp == 8) {
-    bool ok = true;
-    for (int i = 0; i < cnt && ok; ++i) {
-      const int qt = tile0 + i;
-      const int64_t img = ((int64_t)head * a.items + item0 + (qt >> 1)) * 2 + (qt & 1);
-      const int st = i % kWgStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[st], ((i / kWgStages) & 1) ^ 1))) { ok = false; break; }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[st], kTlTile);
-        bulk_load(smem + kWgQ + st * kTlTile, a.q_image + img * kTlTile, kTlTile, &q_full[st]);
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_empty[i & 3], ((i >> 2) & 1) ^ 1))) { ok = false; break; }
-      float4* par = reinterpret_cast<float4*>(smem + kWgPar + (i & 3) * kTlRows * 16);
-      for (int x = lane; x < kTlRows; x += 32) {
-        const int rr = qt * kTlRows + x;
-        float4 v = make_float4(0.f, 0.f, 0.f, __int_as_float(0));
-        if (rr < total) {
-          const float2 s = a.stats[(int64_t)(r0 + rr / a.group) * a.q_heads + head * a.group + rr % a.group];
-          v = make_float4(a.q_coef[img * kTlRows + x], s.x, s.y,
-                          __int_as_float(kv8_visible(a.causal, len, n, rr / a.group)));
-        }
-        par[x] = v;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&par_full[i & 3]);
-    }
-    if (!ok) {   // copies still in flight land in this block's shared memory
-      const uint64_t t = globaltimer_ns();
-      while (globaltimer_ns() - t < 200000ull) {}
-    }
-  } else if (warp == 9) {
-    if (elect_one()) {
-      const uint32_t id = idesc_f16(kTlKeys, kTlRows);
-      const uint32_t kb = smem_u32(smem);
+    if (lane == 0) {
       bool ok = true;
       for (int i = 0; i < cnt && ok; ++i) {
-        const int st = i % kWgStages;
-        if (!mbar_wait(&q_full[st], (i / kWgStages) & 1) || !mbar_wait(&s_empty[i & 3], ((i >> 2) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t qb = smem_u32(smem + kWgQ + st * kTlTile);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
-          mma_bf16_ss(tmem + (i & 3) * 128, smem_desc_kmajor(kb + off, 128), smem_desc_kmajor(qb + off, 128), id, kk > 0);
-        }
-        tc_commit(&s_full[i & 3]);
-        tc_commit(&q_empty[st]);
+        const int qt = tile0 + i, st = i & 1;
+        const int64_t img = ((int64_t)head * a.items + item0 + (qt >> 1)) * 2 + (qt & 1);
+        if (!mbar_wait(&q_empty[st], ((i >> 1) & 1) ^ 1)) { ok = false; break; }
+        // Row slot i % 4 held tile i - 4, whose sums were awaited before the products of tile i - 2, which freed
+        // this stage.
+        mbar_arrive_expect_tx(&q_full[st], kTlTile + kWgRowsBytes);
+        bulk_load(smem + kWgQ + st * kTlTile, a.q_image + img * kTlTile, kTlTile, &q_full[st]);
+        bulk_load(smem + kWgPar + (i & 3) * kWgRowsBytes, a.q_rows + img * 3 * kTlRows, kWgRowsBytes, &q_full[st]);
       }
-      tc_commit(drain);
-      mbar_wait(drain, 0, 100000000ull);
+      if (!ok) {   // copies still in flight land in this block's shared memory
+        const uint64_t t = globaltimer_ns();
+        while (globaltimer_ns() - t < 200000ull) {}
+      }
     }
+    __syncwarp();
+  } else if (warp == 9) {
+    const uint32_t lead = elect_one();
+    constexpr uint32_t id = idesc_f16(kTlKeys, kTlRows);
+    const uint64_t k_desc = smem_desc_kmajor(smem_u32(smem), 128);
+    const uint64_t q_desc = smem_desc_kmajor(smem_u32(smem + kWgQ), 128);
+    for (int i = 0; i < cnt; ++i) {
+      const int st = i & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&q_full[st], (i >> 1) & 1) && mbar_wait(&s_empty[st], ((i >> 1) & 1) ^ 1)))
+        break;
+      tc_fence_after();
+      const uint64_t qd = q_desc + (uint32_t)st * (kTlTile >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off = ((uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u) >> 4;
+        mma_f16_ss_if(lead, tmem + st * 128, k_desc + off, qd + off, id, kk > 0);
+      }
+      tc_commit_if(lead, &s_full[st]);
+      tc_commit_if(lead, &q_empty[st]);
+    }
+    tc_commit_if(lead, drain);
+    mbar_wait(drain, 0, 100000000ull);
     __syncwarp();
   }
   float acc = 0.f;
@@ -778,46 +812,95 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       const int page = kv8_page(c, b, key / kKv8Page);
       if (page >= 0) sk = c.scales[kv8_scale(c, page, head, 0)];
     }
+    const uint64_t sk2 = pack_f32(sk, sk);
     const uint32_t lane_addr = (32u * (uint32_t)(warp & 3)) << 16;
-    for (int i = warp >> 2; i < cnt; i += 2) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&par_full[i & 3], (i >> 2) & 1) && mbar_wait(&s_full[i & 3], (i >> 2) & 1))) {
+    const int st = warp >> 2;                                  // this warpgroup's slot and TMEM buffer
+    for (int i = st; i < cnt; i += 2) {
+      const float* par = reinterpret_cast<const float*>(smem + kWgPar) + (i & 3) * 3 * kTlRows;
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[st], (i >> 1) & 1))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const float4* par = reinterpret_cast<const float4*>(smem + kWgPar + (i & 3) * kTlRows * 16);
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      // rows come in the order of their tokens: if the tile's first row sees the block's last key, all do (rows behind
+      // the last have c = -inf)
+      const bool all_seen = reinterpret_cast<const int*>(par)[2 * kTlRows] >= k0 + kTlKeys;
+      uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t s[32];
-        tmem_ld32(tmem + lane_addr + (i & 3) * 128 + 32 * q, s);
+        tmem_ld32(tmem + lane_addr + st * 128 + 32 * q, s);
         tmem_wait_ld();
         tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(s));
         tmem_reg_fence(*reinterpret_cast<uint32_t(*)[16]>(s + 16));
+        const float4* f4 = reinterpret_cast<const float4*>(par + 32 * q);
+        const float4* k4 = reinterpret_cast<const float4*>(par + kTlRows + 32 * q);
+        const int4* n4 = reinterpret_cast<const int4*>(reinterpret_cast<const int*>(par) + 2 * kTlRows + 32 * q);
+        auto sum = [&](auto every) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float4 v = par[32 * q + e];
-          const float p = ex2(fmaf(__uint_as_float(s[e]) * sk, v.x, -v.y)) * v.z;
-          part[e & 3] += key < __float_as_int(v.w) ? p : 0.f;
-        }
+          for (int e = 0; e < 32; e += 4) {
+            const float4 f = f4[e >> 2], k = k4[e >> 2];
+            uint64_t x01 = fma_f32x2(fma_f32x2(pack_f32(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sk2, 0ull),
+                                     pack_f32(f.x, f.y), pack_f32(k.x, k.y));
+            uint64_t x23 = fma_f32x2(fma_f32x2(pack_f32(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), sk2, 0ull),
+                                     pack_f32(f.z, f.w), pack_f32(k.z, k.w));
+            float p[4];
+            unpack_f32(x01, p[0], p[1]);
+            unpack_f32(x23, p[2], p[3]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (e % 8 == 0 || x < 2) p[x] = ex2(p[x]);
+            if (e % 8 != 0) ex2_poly(p[2], p[3]);
+            if (!decltype(every)::value) {
+              const int4 v = n4[e >> 2];
+              p[0] = key < v.x ? p[0] : 0.f;
+              p[1] = key < v.y ? p[1] : 0.f;
+              p[2] = key < v.z ? p[2] : 0.f;
+              p[3] = key < v.w ? p[3] : 0.f;
+            }
+            sums[0] = add_f32x2(sums[0], pack_f32(p[0], p[1]));
+            sums[1] = add_f32x2(sums[1], pack_f32(p[2], p[3]));
+          }
+        };
+        if (all_seen) sum(std::true_type{});
+        else sum(std::false_type{});
       }
-      acc += (part[0] + part[1]) + (part[2] + part[3]);
+      float x, y;
+      unpack_f32(add_f32x2(sums[0], sums[1]), x, y);
+      acc += x + y;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_empty[i & 3]);
+      if (lane == 0) mbar_arrive(&s_empty[st]);
     }
     if (warp >= 4) reinterpret_cast<float*>(smem + kWgSum)[tid - 128] = acc;
   }
   tc_fence_before();
   __syncthreads();
   if (warp < 4 && ok && k0 + tid < len) {
-    const int64_t at = b * w_seq + head * w_head + k0 + tid;
-    w_out[at] = w_in[at] + (acc + reinterpret_cast<const float*>(smem + kWgSum)[tid]);
+    acc += reinterpret_cast<const float*>(smem + kWgSum)[tid];
+    if (part_out) {
+      part_out[(((int64_t)part * c.seqs + b) * c.heads + head) * a.max_len + k0 + tid] = acc;
+    } else {
+      const int64_t at = b * w_seq + head * w_head + k0 + tid;
+      w_out[at] = w_in[at] + acc;
+    }
   }
   if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
+}
+
+// weights_out = weights_in + the parts' sums, in order: a thread per key.
+__global__ void __launch_bounds__(256)
+    kv8_weigh_add_kernel(const Kv8View c, const Kv8AttnArgs a, const float* w_in, float* w_out, int64_t w_seq,
+                         int64_t w_head, const float* part_out, int parts) {
+  const int b = blockIdx.z, head = blockIdx.y, t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= kv8_len(c, a, b)) return;
+  float acc = 0.f;
+  for (int r = 0; r < parts; ++r) acc += part_out[(((int64_t)r * c.seqs + b) * c.heads + head) * a.max_len + t];
+  const int64_t at = b * w_seq + head * w_head + t;
+  w_out[at] = w_in[at] + acc;
 }
 
 // ---------------------------------------------------------------------------
@@ -825,16 +908,17 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 // ---------------------------------------------------------------------------
 // How a call runs, from its sizes alone (the workspace is sized by the same rule).
 struct Kv8Plan {
-  bool stream;
+  int nq;              // streaming kernel with 8 nq rows a block; 0: the tile kernel
   int items, nsplit;
   bool prepare;        // operand images
   int image_steps;     // 128-key steps of a sequence in them
-  int64_t part_o, part_ml, stats, logits, q_image, q_coef, kv_image, kv_scale, bytes;   // workspace offsets, -1 for none
+  int parts;           // parts of a key block's query tiles
+  int64_t part_o, part_ml, stats, logits, q_image, q_rows, kv_image, kv_scale, w_part, bytes;   // workspace offsets, -1 for none
   int64_t logit_ld;
 };
 
 // Query rows that share a key/value head, per sequence, up to which the streaming kernel runs.
-constexpr int kStreamRows = 32;
+constexpr int kStreamRows = 16;
 // Operand images are made when a key is used by at least this many blocks on average, and fit in this much.
 constexpr int kPrepareItems = 3;
 constexpr int64_t kPrepareBytes = (int64_t)1 << 31;
@@ -843,19 +927,19 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   Kv8Plan p{};
   const int group = q_heads / heads;
   const int64_t packed = (int64_t)rows * group;
-  p.stream = packed <= (int64_t)kStreamRows * seqs;
-  const int unit = p.stream ? kStRows : 2 * kTlRows;
+  p.nq = packed <= 8 * (int64_t)seqs ? 1 : packed <= (int64_t)kStreamRows * seqs ? 2 : 0;
+  const int unit = p.nq ? 8 * p.nq : 2 * kTlRows;
   const int busy = std::min(seqs, rows);             // sequences that can have queries
   p.items = (int)std::min<int64_t>(packed, packed / unit + busy);
   const int64_t blocks = (int64_t)p.items * heads;
   const int steps = std::max(1, (max_len + kTlKeys - 1) / kTlKeys);
   // A split costs its partial result and, with tiles, another setup of the block: the streaming kernel splits until
   // the blocks fill the device four times over, the tile kernel only to fill it once.  At least four steps each.
-  const int64_t fill = p.stream ? (148 * 4 + blocks - 1) / blocks : 148 / std::max<int64_t>(blocks, 1);
+  const int64_t fill = p.nq ? (148 * 4 + blocks - 1) / blocks : 148 / std::max<int64_t>(blocks, 1);
   p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({fill, steps / 4, 64}));
   p.image_steps = steps;
   const int64_t images = (int64_t)seqs * steps * heads;
-  p.prepare = !p.stream && p.items >= kPrepareItems * (int64_t)busy && images * 2 * kTlTile <= kPrepareBytes;
+  p.prepare = p.nq == 0 && p.items >= kPrepareItems * (int64_t)busy && images * 2 * kTlTile <= kPrepareBytes;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -867,11 +951,15 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   p.part_ml = p.nsplit > 1 ? take(fr * p.nsplit * 8) : -1;
   p.stats = weigh ? take(fr * 8) : -1;
   p.logit_ld = (max_len + kKv8Page - 1) / kKv8Page * (int64_t)kKv8Page;
-  p.logits = weigh && p.stream ? take(fr * p.logit_ld * 4) : -1;
-  p.q_image = weigh && !p.stream ? take((int64_t)heads * p.items * 2 * kTlTile) : -1;
-  p.q_coef = weigh && !p.stream ? take((int64_t)heads * p.items * 2 * kTlRows * 4) : -1;
+  p.logits = weigh && p.nq ? take(fr * p.logit_ld * 4) : -1;
+  p.q_image = weigh && p.nq == 0 ? take((int64_t)heads * p.items * 2 * kTlTile) : -1;
+  p.q_rows = weigh && p.nq == 0 ? take((int64_t)heads * p.items * 2 * kTlRows * 12) : -1;
   p.kv_image = p.prepare ? take(images * 2 * kTlTile) : -1;
   p.kv_scale = p.prepare ? take(images * 2 * 16) : -1;
+  // parts: at least eight query tiles each, until the blocks fill the device (two an SM) three times over
+  p.parts = (int)std::max<int64_t>(
+      1, std::min<int64_t>({(148 * 6 + images - 1) / std::max<int64_t>(images, 1), packed / (8 * kTlRows * (int64_t)busy), 8}));
+  p.w_part = weigh && p.nq == 0 && p.parts > 1 ? take(p.parts * (int64_t)seqs * heads * max_len * 4) : -1;
   p.bytes = at;
   return p;
 }
@@ -881,16 +969,25 @@ int64_t kv8_attn_workspace_bytes(int seqs, int heads, int q_heads, int rows, int
 }
 
 namespace {
+template <int FMT, int NQ>
+cudaError_t launch_stream(const dim3& grid, const Kv8View& c, const Kv8AttnArgs& a, cudaStream_t st) {
+  using Sh = StreamShape<NQ>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv8_stream_kernel<FMT, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  if (e != cudaSuccess) return e;
+  kv8_stream_kernel<FMT, NQ><<<grid, Sh::kThreads, Sh::kSmem, st>>>(c, a);
+  return cudaSuccess;
+}
+
 template <int FMT>
 cudaError_t launch_kv8_attn_fmt(const Kv8View& c, const Kv8AttnArgs& a, const Kv8Plan& p, const float* w_in,
-                                float* w_out, int64_t w_seq, int64_t w_head, cudaStream_t st) {
+                                float* w_out, int64_t w_seq, int64_t w_head, void* work, cudaStream_t st) {
   cudaError_t e;
   if (a.rows > 0) {
     const dim3 grid(p.items, c.heads, p.nsplit);
-    if (p.stream) {
-      e = cudaFuncSetAttribute(kv8_stream_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStSmem);
+    if (p.nq) {
+      e = p.nq == 1 ? launch_stream<FMT, 1>(grid, c, a, st) : launch_stream<FMT, 2>(grid, c, a, st);
       if (e != cudaSuccess) return e;
-      kv8_stream_kernel<FMT><<<grid, kStThreads, kStSmem, st>>>(c, a);
     } else {
       if (p.prepare) {
         kv8_prepare_kernel<FMT><<<dim3(p.image_steps, c.heads, c.seqs), 256, 0, st>>>(c, a);
@@ -909,14 +1006,19 @@ cudaError_t launch_kv8_attn_fmt(const Kv8View& c, const Kv8AttnArgs& a, const Kv
     }
   }
   if (w_out && a.max_len > 0) {
-    if (p.stream) {
+    if (p.nq) {
       kv8_weigh_logits_kernel<<<dim3((a.max_len + 255) / 256, c.heads, c.seqs), 256, 0, st>>>(c, a, w_in, w_out, w_seq,
                                                                                               w_head);
     } else {
+      if (p.items > 0) kv8_rows_kernel<<<dim3(p.items, c.heads), 2 * kTlRows, 0, st>>>(c, a);
       e = cudaFuncSetAttribute(kv8_weigh_tile_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWgSmem);
       if (e != cudaSuccess) return e;
-      kv8_weigh_tile_kernel<FMT><<<dim3((a.max_len + kTlKeys - 1) / kTlKeys, c.heads, c.seqs), kWgThreads, kWgSmem,
-                                   st>>>(c, a, w_in, w_out, w_seq, w_head);
+      float* part_out = p.w_part < 0 ? nullptr : reinterpret_cast<float*>(static_cast<uint8_t*>(work) + p.w_part);
+      kv8_weigh_tile_kernel<FMT><<<(unsigned)((int64_t)p.image_steps * c.heads * c.seqs * p.parts), kWgThreads, kWgSmem,
+                                   st>>>(c, a, w_in, w_out, w_seq, w_head, part_out, p.parts);
+      if (part_out)
+        kv8_weigh_add_kernel<<<dim3((a.max_len + 255) / 256, c.heads, c.seqs), 256, 0, st>>>(c, a, w_in, w_out, w_seq,
+                                                                                           w_head, part_out, p.parts);
     }
   }
   return cudaGetLastError();
@@ -952,12 +1054,12 @@ cudaError_t launch_kv8_attn(const Kv8View& c, bool e4m3, const int32_t* lens, co
   a.logits = reinterpret_cast<float*>(at(p.logits));
   a.logit_ld = p.logit_ld;
   a.q_image = at(p.q_image);
-  a.q_coef = reinterpret_cast<float*>(at(p.q_coef));
+  a.q_rows = reinterpret_cast<float*>(at(p.q_rows));
   a.kv_image = at(p.kv_image);
   a.kv_scale = reinterpret_cast<float4*>(at(p.kv_scale));
   a.image_steps = p.image_steps;
-  return e4m3 ? launch_kv8_attn_fmt<RBD_CODES_E4M3>(c, a, p, w_in, w_out, w_seq, w_head, st)
-              : launch_kv8_attn_fmt<RBD_CODES_INT8>(c, a, p, w_in, w_out, w_seq, w_head, st);
+  return e4m3 ? launch_kv8_attn_fmt<RBD_CODES_E4M3>(c, a, p, w_in, w_out, w_seq, w_head, work, st)
+              : launch_kv8_attn_fmt<RBD_CODES_INT8>(c, a, p, w_in, w_out, w_seq, w_head, work, st);
 }
 
 }  // namespace rbd

@@ -152,7 +152,9 @@ class Int8KVCache:
         if pages <= 0:
             raise ValueError("pages must be positive")
         self.sequences, self.max_tokens, self.heads, self.code_format = sequences, max_tokens, heads, code_format
-        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        dev = torch.device(device) if device is not None else torch.device("cuda")
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
         self.codes = torch.zeros((pages, heads, 2, self.PAGE, 128), dtype=torch.uint8, device=dev)
         self.scales = torch.ones((pages, heads, 2), dtype=torch.float32, device=dev)
         # one buffer, so that a step's bookkeeping is one copy (of a pageable host mirror, which the runtime has
@@ -167,6 +169,9 @@ class Int8KVCache:
         self._pages: List[List[int]] = [[] for _ in range(n)]
         self._free = list(range(pages - 1, -1, -1))
         self._lens = [0] * n
+        self._view = B._kv8(self.table, self.codes, self.scales, code_format, dev.index) if dev.type == "cuda" else None
+        self._before_at, self._lens_at, self._cu_at = (t.data_ptr() for t in (self._before, self.device_lens, self._cu))
+        self._work_bytes = {}        # scratch of an attend by its sizes
         self._rows = None            # rows of the prepared step, None when nothing is prepared
         self._may_append = False
 
@@ -216,6 +221,13 @@ class Int8KVCache:
         self._upload(before, counts)
         self._rows, self._may_append = sum(counts), append
 
+    def _current(self) -> int:
+        """The cache's device, which has to be the current one (its kernels run there)."""
+        cur = torch.cuda.current_device()
+        if self.codes.get_device() != cur:
+            raise ValueError(f"cache on {self.codes.device} while cuda:{cur} is current")
+        return cur
+
     def _prepared(self, rows: int) -> None:
         if self._rows is None:
             raise ValueError("prepare() first")
@@ -240,7 +252,7 @@ class Int8KVCache:
         self._prepared(k.shape[0])
         if not self._may_append:
             raise ValueError("prepared without append")
-        B.rbd_kv8_append(k, v, self._cu, self._before, self.table, self.codes, self.scales, self.code_format)
+        B._kv8_append(self._view, self._current(), self._before_at, self._cu_at, k, v)
 
     def attend(self, q: torch.Tensor, heads: int, causal: bool = True, out: Optional[torch.Tensor] = None,
                softmax_scale: float = 128 ** -0.5, weights: Optional[torch.Tensor] = None,
@@ -254,17 +266,22 @@ class Int8KVCache:
             raise ValueError("heads must be a multiple of the cache's heads")
         if q.device != self.codes.device:
             raise ValueError(f"q is on {q.device}, the cache on {self.codes.device}")
+        cur = self._current()
         if out is None:
             out = torch.empty((q.shape[0], heads * 128), dtype=torch.bfloat16, device=q.device)
-        if weights is not None and weights_out is None:
+        if weights_out is None:
             weights_out = weights
         # a capture outlives these lengths: lay it out for any
         longest = self.max_tokens if torch.cuda.is_current_stream_capturing() else max(self._lens)
-        need = B.rbd_kv8_attn_workspace_bytes(self.sequences, self.heads, heads, q.shape[0], longest,
-                                              weights is not None)
+        sizes = (heads, q.shape[0], longest, weights is not None)
+        need = self._work_bytes.get(sizes)
+        if need is None:
+            if len(self._work_bytes) >= 4096:
+                self._work_bytes.clear()
+            need = self._work_bytes[sizes] = B.rbd_kv8_attn_workspace_bytes(self.sequences, self.heads, *sizes)
         work = torch.empty((need,), dtype=torch.uint8, device=q.device) if need > 0 else None
-        B.rbd_kv8_attn(q, self._cu, self.device_lens, self.table, self.codes, self.scales, out, heads, work, longest,
-                       causal, softmax_scale, weights, weights_out, self.code_format)
+        B._kv8_attn(self._view, cur, self._lens_at, self._cu_at, q, out, heads, work, longest, causal, softmax_scale,
+                    weights, weights_out)
         return out
 
     def tail(self, tokens: int) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -274,7 +291,7 @@ class Int8KVCache:
             raise ValueError("tokens must not be negative")
         k = torch.empty((self.sequences, tokens, self.heads * 128), dtype=torch.bfloat16, device=self.codes.device)
         v = torch.empty_like(k)
-        B.rbd_kv8_read(self.device_lens, self.table, self.codes, self.scales, k, v, self.code_format)
+        B._kv8_read(self._view, self._current(), self._lens_at, k, v)
         return k, v
 
     def read(self, sequence: int, first: int = 0, count: Optional[int] = None) -> Tuple[torch.Tensor, torch.Tensor]:
