@@ -640,7 +640,7 @@ rbd_status rbd_kv8_append(const rbd_kv8* cache, const int32_t* lens, const int32
   const rbd_status s = kv8_view(cache, &c, &e4m3);
   if (s != RBD_OK) return s;
   if (rows < 0) return RBD_ERR_INVALID_ARG;
-  if (rows > (1 << 28)) return RBD_ERR_UNSUPPORTED;
+  if (rows > (1 << 28) || rows > ((int64_t)1 << 30) / c.heads) return RBD_ERR_UNSUPPORTED;   // grid of pages x heads
   if (rows == 0 || c.seqs == 0) return RBD_OK;
   if (!lens || !cu || !k || !v || ldk < (int64_t)c.heads * 128 || ldv < (int64_t)c.heads * 128)
     return RBD_ERR_INVALID_ARG;

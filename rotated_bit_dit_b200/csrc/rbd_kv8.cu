@@ -31,17 +31,18 @@ __device__ __forceinline__ uint32_t finite_amax(uint32_t m, uint32_t w) {
 
 template <int FMT>
 __device__ __forceinline__ uint32_t encode_bf16x4(uint32_t w0, uint32_t w1, float inv) {
-  return kv8_encode1<FMT>(bf16_lo(w0), inv) | (kv8_encode1<FMT>(bf16_hi(w0), inv) << 8) |
-         (kv8_encode1<FMT>(bf16_lo(w1), inv) << 16) | (kv8_encode1<FMT>(bf16_hi(w1), inv) << 24);
+  const float x[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)};
+  return kv8_encode4<FMT, true>(x, inv);
 }
 
-// Code of a stored code under a new scale: the value it stands for, quantised again.
+// Codes of four stored codes under a new scale: the values they stand for, quantised again.
 template <int FMT>
 __device__ __forceinline__ uint32_t requantise4(uint32_t w, float s_old, float inv) {
-  uint32_t o = 0;
+  float v[4];
+  kv8_decode4<FMT>(w, v);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o |= kv8_encode1<FMT>(__fmul_rn(kv8_decode1<FMT>(w, j), s_old), inv) << (8 * j);
-  return o;
+  for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(v[j], s_old);
+  return kv8_encode4<FMT, false>(v, inv);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -55,6 +56,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // Thread l of a side takes 8 channels (16 bytes of bf16) of rows l / 16, l / 16 +
 // 8, ...: the page's new values stay in registers between the maximum and the
 // codes, so they are read once.  Bound by memory: 2 bytes in, 1 byte out a value.
+// Heads are the fastest index of the blocks: those that run together then read whole
+// rows of k and v, not 256 bytes of each.
 template <int FMT>
 __global__ void __launch_bounds__(256)
     kv8_append_kernel(const Kv8View c, const int32_t* __restrict__ lens, const int32_t* __restrict__ cu,
@@ -72,13 +75,11 @@ __global__ void __launch_bounds__(256)
     return (len + n - 1) / kKv8Page - len / kKv8Page + 1;
   };
   int b, idx;
-  if (!kv8_find(c.seqs, blockIdx.x, pages_of, b, idx)) return;
-  const int head = blockIdx.y;
+  if (!kv8_find(c.seqs, blockIdx.x / c.heads, pages_of, b, idx)) return;
+  const int head = blockIdx.x % c.heads;
   const int len = __ldg(lens + b);
   const int r0 = __ldg(cu + b), n = __ldg(cu + b + 1) - r0;
   const int p = len / kKv8Page + idx;
-  const int page = kv8_page(c, b, p);
-  if (page < 0) return;
   const int held = max(0, len - p * kKv8Page);                       // rows that already hold tokens
   const int end = min(kKv8Page, len + n - p * kKv8Page);             // rows held afterwards
   const int side = threadIdx.x >> 7, tid = threadIdx.x & 127;
@@ -97,6 +98,8 @@ __global__ void __launch_bounds__(256)
       raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (first + t) * ld + head * kKv8Dim + 8 * chunk8));
     m = finite_amax(finite_amax(finite_amax(finite_amax(m, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
   }
+  const int page = kv8_page(c, b, p);            // (after the loads above: none waits for it)
+  if (page < 0) return;
   float* scale = c.scales + kv8_scale(c, page, head, side);
   const float s_old = held > 0 ? *scale : kKv8Floor;
   m = __reduce_max_sync(0xffffffffu, m);
@@ -121,43 +124,57 @@ __global__ void __launch_bounds__(256)
   if (tid == 0) *scale = s;
 }
 
-// The last `tokens` tokens of every sequence as bf16 rows [seqs * tokens]: a thread
-// per (row, head, 16-channel chunk), both sides.  Bound by memory: 1 byte in, 2 out.
+// The last `tokens` tokens of every sequence as bf16 rows [seqs * tokens].  A block
+// takes 16 rows and up to 4 heads, a thread one side's 16-channel chunk of a row in
+// each head: pages are read 2 KB at a time, all four loads in flight.  Bound by
+// memory: 1 byte in, 2 out.
+constexpr int kRdRows = 16, kRdHeads = 4;
 template <int FMT>
 __global__ void __launch_bounds__(256)
-    kv8_read_kernel(const Kv8View c, const int32_t* __restrict__ lens, int tokens, int64_t units,
-                    uint16_t* __restrict__ k, int64_t ldk, uint16_t* __restrict__ v, int64_t ldv) {
-  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (u >= units) return;
-  const int chunk = (int)(u & 7);
-  const int64_t rh = u >> 3;
-  const int64_t row = rh / c.heads;
-  const int head = (int)(rh - row * c.heads);
-  const int b = (int)(row / tokens);
-  const int i = (int)(row - (int64_t)b * tokens);
+    kv8_read_kernel(const Kv8View c, const int32_t* __restrict__ lens, int tokens, uint16_t* __restrict__ k,
+                    int64_t ldk, uint16_t* __restrict__ v, int64_t ldv) {
+  const int chunk = threadIdx.x & 7, side = (threadIdx.x >> 3) & 1;
+  const int groups = (c.heads + kRdHeads - 1) / kRdHeads;
+  const int head0 = (int)(blockIdx.x % groups) * kRdHeads;
+  const int64_t block = blockIdx.x / groups;
+  const int per = (tokens + kRdRows - 1) / kRdRows;
+  const int b = (int)(block / per);
+  const int i = (int)(block - (int64_t)b * per) * kRdRows + (threadIdx.x >> 4);
+  if (i >= tokens) return;
   const int len = __ldg(lens + b);
   const int64_t t = (int64_t)len - tokens + i;
   int page = -1;
   if (len < 0 || len > c.max_pages * kKv8Page) record_refusal();
   else if (t >= 0) page = kv8_page(c, b, (int)(t / kKv8Page));
+  uint4 w[kRdHeads];
+  float s[kRdHeads];
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    float s = 0.f;
-    if (page >= 0) {
-      w = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, page, head, side) +
-                                          kv8_chunk((int)(t % kKv8Page), chunk));
-      s = c.scales[kv8_scale(c, page, head, side)];
+  for (int h = 0; h < kRdHeads; ++h) {
+    w[h] = make_uint4(0u, 0u, 0u, 0u);
+    s[h] = 0.f;
+    if (page >= 0 && head0 + h < c.heads) {
+      w[h] = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, page, head0 + h, side) +
+                                             kv8_chunk((int)(t % kKv8Page), chunk));
+      s[h] = c.scales[kv8_scale(c, page, head0 + h, side)];
     }
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  }
+  const int64_t row = (int64_t)b * tokens + i;
+  uint16_t* dst = (side ? v + row * ldv : k + row * ldk) + 16 * chunk;
+#pragma unroll
+  for (int h = 0; h < kRdHeads; ++h) {
+    if (head0 + h >= c.heads) break;
+    const uint32_t ws[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
     uint32_t o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      o[j] = pack_bf16(__fmul_rn(kv8_decode1<FMT>(ws[j >> 1], 2 * (j & 1)), s),
-                       __fmul_rn(kv8_decode1<FMT>(ws[j >> 1], 2 * (j & 1) + 1), s));
-    uint4* dst = reinterpret_cast<uint4*>((side ? v + row * ldv : k + row * ldk) + head * kKv8Dim + 16 * chunk);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int j = 0; j < 4; ++j) {
+      float x[4];
+      kv8_decode4<FMT>(ws[j], x);
+      o[2 * j] = pack_bf16(__fmul_rn(x[0], s[h]), __fmul_rn(x[1], s[h]));
+      o[2 * j + 1] = pack_bf16(__fmul_rn(x[2], s[h]), __fmul_rn(x[3], s[h]));
+    }
+    uint4* out = reinterpret_cast<uint4*>(dst + (head0 + h) * kKv8Dim);
+    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -203,6 +220,8 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8View c
   __shared__ uint32_t sh_bin, sh_above;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y, head = blockIdx.x;
+  // sum of the warps' values in front of this warp's
+  auto sum_before = [&](const uint32_t* v) { return __reduce_add_sync(0xffffffffu, lane < warp ? v[lane] : 0u); };
   int n = __ldg(a.lens + b);
   if (n < 0 || n > a.width || n > c.max_pages * kKv8Page) {
     if (tid == 0) record_refusal();
@@ -217,7 +236,15 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8View c
     const int cand = n - a.recent;          // positions that compete
     int want = a.keep - a.recent;           // how many of them stay
     for (int j = tid; j < a.recent; j += kSelThreads) kept[want + j] = cand + j;
-    for (int i = tid; i < cand && i < cap; i += kSelThreads) keys[i] = order_key(__ldg(w + i));
+    const int cached = min(cand, cap);
+    for (int i0 = tid; i0 < cached; i0 += 8 * kSelThreads) {        // eight loads in flight
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = i0 + u * kSelThreads < cached ? __ldg(w + i0 + u * kSelThreads) : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u * kSelThreads < cached) keys[i0 + u * kSelThreads] = order_key(x[u]);
+    }
     auto key = [&](int i) { return i < cap ? keys[i] : order_key(__ldg(w + i)); };
     uint32_t prefix = 0, mask = 0;
     uint32_t eq_want = (uint32_t)want;      // of the keys under the prefix, how many stay
@@ -243,9 +270,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8View c
         }
         if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
-        uint32_t before = 0;
-        for (int i = 0; i < warp; ++i) before += warp_sum[i];
-        const uint32_t excl = before + incl - (h0 + h1);
+        const uint32_t excl = sum_before(warp_sum) + incl - (h0 + h1);
         if (excl < eq_want && eq_want <= excl + h0 + h1) {
           const bool second = eq_want > excl + h0;
           sh_bin = (uint32_t)(kSelBins - 1 - 2 * tid - (second ? 1 : 0));
@@ -271,11 +296,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8View c
         warp_eq[warp] = eq;
       }
       __syncthreads();
-      uint32_t at_gt = 0, at_eq = 0;
-      for (int i = 0; i < warp; ++i) {
-        at_gt += warp_sum[i];
-        at_eq += warp_eq[i];
-      }
+      uint32_t at_gt = sum_before(warp_sum), at_eq = sum_before(warp_eq);
       const uint32_t below = (1u << lane) - 1u;
       for (int i = i0; i < i1; i += 32) {
         const uint32_t u = i + lane < i1 ? key(i + lane) : 0u;
@@ -293,11 +314,14 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8View c
   // weights of the kept tokens, ascending; safe in place, since position j never comes from below j and a
   // chunk is read before it is written
   float* wo = a.weights_out + b * a.o_seq + head * a.o_head;
-  for (int j0 = 0; j0 < m; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const float x = j < m ? w[kept[j]] : 0.f;
+  for (int j0 = tid; j0 - tid < m; j0 += 4 * kSelThreads) {
+    float x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = j0 + u * kSelThreads < m ? w[kept[j0 + u * kSelThreads]] : 0.f;
     __syncthreads();
-    if (j < m) wo[j] = x;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (j0 + u * kSelThreads < m) wo[j0 + u * kSelThreads] = x[u];
     __syncthreads();
   }
   for (int j = m + tid; j < a.width_out; j += kSelThreads) wo[j] = 0.f;
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8View c
 // 0-127 the keys, 128-255 the values, 16 channels of 4 rows each, read once and
 // kept in registers between the maximum and the new codes.
 template <int FMT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     kv8_gather_kernel(const Kv8View c, const int32_t* __restrict__ dst_table, int64_t ld_dst,
                       const int32_t* __restrict__ kept, const int32_t* __restrict__ lens_out, int keep) {
   __shared__ uint32_t red[2][4];
@@ -345,9 +369,26 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t ws[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    float top = 0.f;
+    float top;                                                  // largest |code| of the sixteen
+    if (FMT == RBD_CODES_INT8) {
+      __half2 t = __float2half2_rn(0.f);                        // codes are exact in fp16
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(kv8_decode1<FMT>(ws[j >> 2], j & 3)));
+      for (int j = 0; j < 4; ++j) {
+        uint32_t p0, p1;
+        kv8_to_f16<FMT>(ws[j], p0, p1);
+        t = __hmax2(t, __hmax2(__habs2(*reinterpret_cast<__half2*>(&p0)), __habs2(*reinterpret_cast<__half2*>(&p1))));
+      }
+      const float2 t2 = __half22float2(t);
+      top = fmaxf(t2.x, t2.y);
+    } else {
+      uint32_t t = 0;                                           // E4M3 magnitudes order like their bytes
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        t = __vmaxu2(t, __vmaxu2(ws[j] & 0x007F007Fu, (ws[j] >> 8) & 0x007F007Fu));
+      float v[4];
+      kv8_decode4<FMT>(max(t & 0xFFu, t >> 16), v);
+      top = v[0];
+    }
     am = fmaxf(am, __fmul_rn(top, s_src[i]));
   }
   const uint32_t m_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
@@ -375,7 +416,7 @@ cudaError_t launch_kv8_append(const Kv8View& c, bool e4m3, const int32_t* lens, 
                               int64_t ldk, const uint16_t* v, int64_t ldv, int rows, cudaStream_t st) {
   // n tokens touch at most (n - 1) / 64 + 2 pages; never more than one page a token
   const int64_t items = std::min<int64_t>(rows, (int64_t)rows / kKv8Page + 2 * (int64_t)std::min(c.seqs, rows));
-  const dim3 grid((unsigned)items, c.heads);
+  const unsigned grid = (unsigned)(items * c.heads);
   if (e4m3) kv8_append_kernel<RBD_CODES_E4M3><<<grid, 256, 0, st>>>(c, lens, cu, k, ldk, v, ldv, rows);
   else kv8_append_kernel<RBD_CODES_INT8><<<grid, 256, 0, st>>>(c, lens, cu, k, ldk, v, ldv, rows);
   return cudaGetLastError();
@@ -383,10 +424,10 @@ cudaError_t launch_kv8_append(const Kv8View& c, bool e4m3, const int32_t* lens, 
 
 cudaError_t launch_kv8_read(const Kv8View& c, bool e4m3, const int32_t* lens, int tokens, uint16_t* k, int64_t ldk,
                             uint16_t* v, int64_t ldv, cudaStream_t st) {
-  const int64_t units = (int64_t)c.seqs * tokens * c.heads * 8;
-  const unsigned grid = (unsigned)((units + 255) / 256);
-  if (e4m3) kv8_read_kernel<RBD_CODES_E4M3><<<grid, 256, 0, st>>>(c, lens, tokens, units, k, ldk, v, ldv);
-  else kv8_read_kernel<RBD_CODES_INT8><<<grid, 256, 0, st>>>(c, lens, tokens, units, k, ldk, v, ldv);
+  const unsigned grid = (unsigned)((int64_t)c.seqs * ((tokens + kRdRows - 1) / kRdRows) *
+                                   ((c.heads + kRdHeads - 1) / kRdHeads));
+  if (e4m3) kv8_read_kernel<RBD_CODES_E4M3><<<grid, 256, 0, st>>>(c, lens, tokens, k, ldk, v, ldv);
+  else kv8_read_kernel<RBD_CODES_INT8><<<grid, 256, 0, st>>>(c, lens, tokens, k, ldk, v, ldv);
   return cudaGetLastError();
 }
 

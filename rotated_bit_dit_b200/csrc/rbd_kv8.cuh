@@ -13,7 +13,6 @@
 #pragma once
 
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "rbd_common.cuh"
 
@@ -99,25 +98,29 @@ __host__ __device__ __forceinline__ constexpr float kv8_inv_qmax() {
   return FMT == RBD_CODES_INT8 ? 1.f / 127.f : 1.f / 448.f;
 }
 
-// Code of x under the inverse scale inv; a NaN is stored as zero, an infinity as the largest code.
-template <int FMT>
-__device__ __forceinline__ uint32_t kv8_encode1(float x, float inv) {
-  const float y = __fmul_rn(x, inv);
-  if (FMT == RBD_CODES_INT8) {
-    int q = __float2int_rn(y);                      // saturates; NaN gives 0
-    q = q > 127 ? 127 : (q < -127 ? -127 : q);
-    return (uint32_t)q & 0xFFu;
+// Code bytes of four values x under the inverse scale inv.  RAW: the values come from a caller, whose NaN is stored
+// as zero (an infinity becomes the largest code).  INT8 rounds by adding 1.5 * 2^23, whose low byte is then the
+// two's complement code (the conversion instruction runs at an eighth of the rate).
+template <int FMT, bool RAW>
+__device__ __forceinline__ uint32_t kv8_encode4(const float (&x)[4], float inv) {
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    y[j] = __fmul_rn(x[j], inv);
+    if (RAW) y[j] = y[j] == y[j] ? y[j] : 0.f;
   }
-  return y != y ? 0u : (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
-}
-
-// Value of code byte j of word w (0 <= j < 4).
-template <int FMT>
-__device__ __forceinline__ float kv8_decode1(uint32_t w, int j) {
-  const uint32_t byte = (w >> (8 * j)) & 0xFFu;
-  if (FMT == RBD_CODES_INT8) return (float)(int8_t)byte;
-  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3);
-  return __half2float(__half(h));
+  if (FMT == RBD_CODES_INT8) {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(__fadd_rn(fminf(fmaxf(y[j], -127.f), 127.f), 12582912.f));
+    return prmt(prmt(u[0], u[1], 0x0040u), prmt(u[2], u[3], 0x0040u), 0x5410u);
+  }
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(d)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
+  return d;
 }
 
 // Four code bytes -> two fp16 pairs.  INT8: (b0, b2) and (b1, b3); the byte with its sign bit flipped, under the
@@ -142,6 +145,18 @@ __device__ __forceinline__ void kv8_to_f16(uint32_t w, uint32_t& p0, uint32_t& p
     p0 = e4m3x2_to_f16x2(w & 0xFFFFu);
     p1 = e4m3x2_to_f16x2(w >> 16);
   }
+}
+// Four codes as float32, in order.
+template <int FMT>
+__device__ __forceinline__ void kv8_decode4(uint32_t w, float (&v)[4]) {
+  uint32_t p0, p1;
+  kv8_to_f16<FMT>(FMT == RBD_CODES_INT8 ? prmt(w, 0u, 0x3120u) : w, p0, p1);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&p0));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&p1));
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = b.x;
+  v[3] = b.y;
 }
 
 }  // namespace rbd

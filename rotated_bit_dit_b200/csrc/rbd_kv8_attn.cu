@@ -521,21 +521,38 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnArgs a) {
   if (fr >= (int64_t)a.rows * a.q_heads) return;
   const int64_t tok = fr / a.q_heads;
   if (tok < __ldg(a.cu) || tok >= __ldg(a.cu + a.seqs)) return;      // rows of no sequence stay as they are
-  const float2* ml = a.part_ml + fr * a.nsplit;
-  float m = -INFINITY;
-  for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, ml[s].x);
-  float lsum = 0.f;
+  const float2* ml = a.part_ml + fr * a.nsplit;          // at most 64 splits: two a lane
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2 x0 = lane < a.nsplit ? ml[lane] : none, x1 = lane + 32 < a.nsplit ? ml[lane + 32] : none;
+  float m = fmaxf(x0.x, x1.x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  // factor of a split; zero for one without keys, which wrote no O (a NaN sum keeps its NaN)
+  auto factor = [&](const float2& x) { return x.y == 0.f ? 0.f : (x.x > -INFINITY ? ex2(x.x - m) : 1.f); };
+  const float f0 = factor(x0), f1 = factor(x1);
+  float lsum = fmaf(x0.y, f0, x1.y * f1);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float2 x = ml[s];
-    if (x.y == 0.f) continue;                     // a split without keys wrote no O
-    const float f = x.x > -INFINITY ? ex2(x.x - m) : 1.f;
-    const float4 u = *reinterpret_cast<const float4*>(a.part_o + (fr * a.nsplit + s) * kKv8Dim + 4 * lane);
-    lsum = fmaf(x.y, f, lsum);
-    acc.x = fmaf(u.x, f, acc.x);
-    acc.y = fmaf(u.y, f, acc.y);
-    acc.z = fmaf(u.z, f, acc.z);
-    acc.w = fmaf(u.w, f, acc.w);
+  const float4* part = reinterpret_cast<const float4*>(a.part_o + fr * a.nsplit * kKv8Dim) + lane;
+  for (int s0 = 0; s0 < a.nsplit; s0 += 4) {
+    float4 u[4];
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i;
+      const float y = __shfl_sync(0xffffffffu, s < 32 ? x0.y : x1.y, s & 31);
+      f[i] = __shfl_sync(0xffffffffu, s < 32 ? f0 : f1, s & 31);
+      u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < a.nsplit && y != 0.f) u[i] = part[s * (kKv8Dim / 4)];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc.x = fmaf(u[i].x, f[i], acc.x);
+      acc.y = fmaf(u[i].y, f[i], acc.y);
+      acc.z = fmaf(u[i].z, f[i], acc.z);
+      acc.w = fmaf(u[i].w, f[i], acc.w);
+    }
   }
   const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;
   const __nv_bfloat162 p = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), q = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);

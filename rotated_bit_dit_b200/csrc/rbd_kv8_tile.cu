@@ -276,9 +276,9 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
     if (CONV) {
       reg_dec<104>();
       const int w4 = warp - 12;
-      uint4 raw[8];
+      uint4 raw_k[8], raw_v[8];                                  // a step ahead
       float2 sc = make_float2(1.f, 1.f);
-      auto fetch = [&](int side, int j) {
+      auto fetch = [&](int side, int j, uint4 (&raw)[8]) {
         const int p = (j0 + j) * 2 + (w4 >> 1);
         const int held = len - p * kKv8Page;                     // tokens of the page
         const int page = held > 0 ? kv8_page(c, b, p) : -1;
@@ -295,29 +295,32 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
           if (page >= 0) sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page, head, 0));
         }
       };
-      auto put = [&](int side, int j) {
+      auto put = [&](int side, int j, const uint4 (&raw)[8]) {
         unsigned char* dst = smem + (side ? kTlV : kTlK) + (j & 1) * kTlTile;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           store_codes<FMT>(dst, 32 * w4 + 8 * (i >> 1) + (lane >> 2), (lane & 3) + 4 * (i & 1), raw[i]);
       };
-      if (cnt > 0) fetch(0, 0);
+      if (cnt > 0) {
+        fetch(0, 0, raw_k);
+        fetch(1, 0, raw_v);
+      }
       for (int j = 0; j < cnt; ++j) {
         const uint32_t par = ((j >> 1) & 1) ^ 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[j & 1], par))) break;
-        put(0, j);
+        put(0, j, raw_k);
         // Slot j % 4 was last read for step j - 4, whose P V (awaited before its K stage came free for step j - 2)
         // follows that softmax.
         if ((w4 & 1) == 0 && lane == 0)
           *reinterpret_cast<float4*>(smem + kTlScale + (j & 3) * 32 + (w4 >> 1) * 16) =
               make_float4(sc.x, log2f(sc.y), 1.0f / sc.y, 0.f);
-        fetch(1, j);
+        if (j + 1 < cnt) fetch(0, j + 1, raw_k);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[j & 1]);
         if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[j & 1], par))) break;
-        put(1, j);
-        if (j + 1 < cnt) fetch(0, j + 1);
+        put(1, j, raw_v);
+        if (j + 1 < cnt) fetch(1, j + 1, raw_v);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[j & 1]);
@@ -917,8 +920,9 @@ struct Kv8Plan {
   int64_t logit_ld;
 };
 
-// Query rows that share a key/value head, per sequence, up to which the streaming kernel runs.
-constexpr int kStreamRows = 16;
+// Query rows that share a key/value head, per sequence, up to which the streaming kernel runs, 16 to a block (32
+// rows over 3000 keys x 24 x 8: 84 us against the tile kernel's 137; 44 rows: 92 against 100).
+constexpr int kStreamRows = 40;
 // Operand images are made when a key is used by at least this many blocks on average, and fit in this much.
 constexpr int kPrepareItems = 3;
 constexpr int64_t kPrepareBytes = (int64_t)1 << 31;
@@ -933,9 +937,12 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   p.items = (int)std::min<int64_t>(packed, packed / unit + busy);
   const int64_t blocks = (int64_t)p.items * heads;
   const int steps = std::max(1, (max_len + kTlKeys - 1) / kTlKeys);
-  // A split costs its partial result and, with tiles, another setup of the block: the streaming kernel splits until
-  // the blocks fill the device four times over, the tile kernel only to fill it once.  At least four steps each.
-  const int64_t fill = p.nq ? (148 * 4 + blocks - 1) / blocks : 148 / std::max<int64_t>(blocks, 1);
+  // A split costs its partial result and, with tiles, another setup of the block: the streaming kernel splits into
+  // four blocks an SM where there are fewer than two (3 sequences of up to 120001 keys: 104 us, 115 with two a
+  // SM; 24 sequences x 8 heads x 2 blocks: 55 us unsplit, 67 split in two), the tile kernel only to fill the device
+  // once.  At least four 128-key steps each.
+  const int64_t fill = p.nq ? (blocks < 148 * 2 ? (148 * 4 + blocks - 1) / std::max<int64_t>(blocks, 1) : 1)
+                            : 148 / std::max<int64_t>(blocks, 1);
   p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({fill, steps / 4, 64}));
   p.image_steps = steps;
   const int64_t images = (int64_t)seqs * steps * heads;
