@@ -394,9 +394,15 @@ def _at(t: torch.Tensor, cur: int) -> int:
     return t.data_ptr()
 
 
-def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream if not isinstance(stream, int) \
-        else stream
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, cur: int) -> int:
+    """cudaStream_t of `stream`, or of the current stream of device `cur` (without making a Stream object of it,
+    which costs as much as a launch)."""
+    if stream is None:
+        return _current_raw_stream(cur) if _current_raw_stream else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _kv8(table: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, code_format: int, cur: int) -> Kv8:
@@ -445,7 +451,7 @@ def _kv8_append(c: Kv8, cur: int, lens: int, cu: int, k: torch.Tensor, v: torch.
     rows = k.shape[0]
     if rows != v.shape[0]:
         raise ValueError("k and v differ in rows")
-    _ok(load().rbd_kv8_append(c, lens, cu, _at(k, cur), ldk, _at(v, cur), ldv, rows, _raw_stream(stream)),
+    _ok(load().rbd_kv8_append(c, lens, cu, _at(k, cur), ldk, _at(v, cur), ldv, rows, _raw_stream(stream, cur)),
         "rbd_kv8_append")
 
 
@@ -464,7 +470,7 @@ def _kv8_read(c: Kv8, cur: int, lens: int, k: torch.Tensor, v: torch.Tensor, str
     if s != v.shape or len(s) != 3 or s[0] != c.seqs or s[2] != cols or k.dtype != torch.bfloat16 or \
             v.dtype != torch.bfloat16 or not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("k and v must be contiguous bf16 [seqs, tokens, heads*128]")
-    _ok(load().rbd_kv8_read(c, lens, s[1], _at(k, cur), cols, _at(v, cur), cols, _raw_stream(stream)), "rbd_kv8_read")
+    _ok(load().rbd_kv8_read(c, lens, s[1], _at(k, cur), cols, _at(v, cur), cols, _raw_stream(stream, cur)), "rbd_kv8_read")
 
 
 def rbd_kv8_read(lens: torch.Tensor, table: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, k: torch.Tensor,
@@ -501,7 +507,7 @@ def _kv8_attn(c: Kv8, cur: int, lens: int, cu: int, q: torch.Tensor, o: torch.Te
         w_in, w_out = _at(weights_in, cur), _at(weights_out, cur)
     _ok(load().rbd_kv8_attn(c, lens, cu, _at(q, cur), ldq, rows, q_heads, causal, softmax_scale, max_len, _at(o, cur), ldo,
                             w_in, w_out, w_seq, w_head, None if work is None else _at(work, cur),
-                            0 if work is None else work.numel() * work.element_size(), _raw_stream(stream)),
+                            0 if work is None else work.numel() * work.element_size(), _raw_stream(stream, cur)),
         "rbd_kv8_attn")
 
 
@@ -541,7 +547,7 @@ def rbd_kv8_evict(weights: torch.Tensor, lens: torch.Tensor, table: torch.Tensor
     _ok(load().rbd_kv8_evict(c, _i32(lens, c.seqs, "lens", cur), _at(weights, cur), w_seq, w_head, width, keep, recent,
                              _at(dst_table, cur), dst_table.stride(0) if d[0] > 1 else d[1], _at(kept, cur),
                              _at(weights_out, cur), o_seq, o_head, width_out, _i32(lens_out, c.seqs, "lens_out", cur),
-                             _raw_stream(stream)), "rbd_kv8_evict")
+                             _raw_stream(stream, cur)), "rbd_kv8_evict")
 
 
 def rbd_svdquant_fit(w: torch.Tensor, rank: int, omegas, bits: int = 4, rot_group: int = 256, scale_group: int = 0,

@@ -439,8 +439,8 @@ cudaError_t launch_kv8_evict(const Kv8View& c, bool e4m3, const float* weights, 
                        lens,    lens_out, kept, keep,  recent};
   const int cap = std::min(std::min(width, c.max_pages * kKv8Page), kSelMaxKeys);
   const int smem = (kSelBins + cap) * 4;
-  cudaError_t e = cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (kSelBins + kSelMaxKeys) * 4);
+  static SmemAllowance allowed;
+  const cudaError_t e = allowed.raise(kv8_select_kernel, (kSelBins + kSelMaxKeys) * 4);
   if (e != cudaSuccess) return e;
   kv8_select_kernel<<<dim3(c.heads, c.seqs), kSelThreads, smem, st>>>(c, a, cap);
   const dim3 grid((keep + kKv8Page - 1) / kKv8Page, c.heads, c.seqs);

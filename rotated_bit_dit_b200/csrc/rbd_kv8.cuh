@@ -12,6 +12,8 @@
 // [pages][heads][2] float32; value = code * scale.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "rbd_common.cuh"
@@ -23,6 +25,23 @@ namespace rbd {
 // g_device_status, which makes bounded waits give up.
 __device__ int g_device_refusal = 0;
 __device__ __forceinline__ void record_refusal() { atomicCAS(&g_device_refusal, 0, RBD_ERR_INVALID_ARG); }
+
+// Raises a kernel's dynamic shared memory limit once per device (a driver call each time costs a call of these
+// sizes a microsecond).  Setting it twice, from two threads, does no harm.
+struct SmemAllowance {
+  std::atomic<uint64_t> done{0};
+  template <class Kernel>
+  cudaError_t raise(Kernel* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
 
 constexpr int kKv8Page = 64;                       // tokens per page
 constexpr int kKv8Dim = 128;                       // channels per head

@@ -940,10 +940,10 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   // A split costs its partial result and, with tiles, another setup of the block: the streaming kernel splits into
   // four blocks an SM where there are fewer than two (3 sequences of up to 120001 keys: 104 us, 115 with two a
   // SM; 24 sequences x 8 heads x 2 blocks: 55 us unsplit, 67 split in two), the tile kernel only to fill the device
-  // once.  At least four 128-key steps each.
+  // once.  At least eight 128-key steps each.
   const int64_t fill = p.nq ? (blocks < 148 * 2 ? (148 * 4 + blocks - 1) / std::max<int64_t>(blocks, 1) : 1)
                             : 148 / std::max<int64_t>(blocks, 1);
-  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({fill, steps / 4, 64}));
+  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({fill, steps / 8, 64}));
   p.image_steps = steps;
   const int64_t images = (int64_t)seqs * steps * heads;
   p.prepare = p.nq == 0 && p.items >= kPrepareItems * (int64_t)busy && images * 2 * kTlTile <= kPrepareBytes;
@@ -979,8 +979,8 @@ namespace {
 template <int FMT, int NQ>
 cudaError_t launch_stream(const dim3& grid, const Kv8View& c, const Kv8AttnArgs& a, cudaStream_t st) {
   using Sh = StreamShape<NQ>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kv8_stream_kernel<FMT, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  static SmemAllowance allowed;
+  const cudaError_t e = allowed.raise(kv8_stream_kernel<FMT, NQ>, Sh::kSmem);
   if (e != cudaSuccess) return e;
   kv8_stream_kernel<FMT, NQ><<<grid, Sh::kThreads, Sh::kSmem, st>>>(c, a);
   return cudaSuccess;
@@ -998,11 +998,13 @@ cudaError_t launch_kv8_attn_fmt(const Kv8View& c, const Kv8AttnArgs& a, const Kv
     } else {
       if (p.prepare) {
         kv8_prepare_kernel<FMT><<<dim3(p.image_steps, c.heads, c.seqs), 256, 0, st>>>(c, a);
-        e = cudaFuncSetAttribute(kv8_tile_kernel<FMT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTlSmem);
+        static SmemAllowance allowed;
+        e = allowed.raise(kv8_tile_kernel<FMT, false>, kTlSmem);
         if (e != cudaSuccess) return e;
         kv8_tile_kernel<FMT, false><<<grid, kTlThreads, kTlSmem, st>>>(c, a);
       } else {
-        e = cudaFuncSetAttribute(kv8_tile_kernel<FMT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTlSmem);
+        static SmemAllowance allowed;
+        e = allowed.raise(kv8_tile_kernel<FMT, true>, kTlSmem);
         if (e != cudaSuccess) return e;
         kv8_tile_kernel<FMT, true><<<grid, kTlConvThreads, kTlSmem, st>>>(c, a);
       }
@@ -1018,7 +1020,8 @@ cudaError_t launch_kv8_attn_fmt(const Kv8View& c, const Kv8AttnArgs& a, const Kv
                                                                                               w_head);
     } else {
       if (p.items > 0) kv8_rows_kernel<<<dim3(p.items, c.heads), 2 * kTlRows, 0, st>>>(c, a);
-      e = cudaFuncSetAttribute(kv8_weigh_tile_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWgSmem);
+      static SmemAllowance allowed;
+      e = allowed.raise(kv8_weigh_tile_kernel<FMT>, kWgSmem);
       if (e != cudaSuccess) return e;
       float* part_out = p.w_part < 0 ? nullptr : reinterpret_cast<float*>(static_cast<uint8_t*>(work) + p.w_part);
       kv8_weigh_tile_kernel<FMT><<<(unsigned)((int64_t)p.image_steps * c.heads * c.seqs * p.parts), kWgThreads, kWgSmem,

@@ -155,6 +155,7 @@ class Int8KVCache:
         dev = torch.device(device) if device is not None else torch.device("cuda")
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
+        self._device = dev
         self.codes = torch.zeros((pages, heads, 2, self.PAGE, 128), dtype=torch.uint8, device=dev)
         self.scales = torch.ones((pages, heads, 2), dtype=torch.float32, device=dev)
         # one buffer, so that a step's bookkeeping is one copy (of a pageable host mirror, which the runtime has
@@ -224,8 +225,8 @@ class Int8KVCache:
     def _current(self) -> int:
         """The cache's device, which has to be the current one (its kernels run there)."""
         cur = torch.cuda.current_device()
-        if self.codes.get_device() != cur:
-            raise ValueError(f"cache on {self.codes.device} while cuda:{cur} is current")
+        if self._device.index != cur:
+            raise ValueError(f"cache on {self._device} while cuda:{cur} is current")
         return cur
 
     def _prepared(self, rows: int) -> None:
@@ -241,8 +242,8 @@ class Int8KVCache:
         for t in (k, v):
             if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] < self.heads * 128 or t.stride(1) != 1:
                 raise ValueError("k and v must be bf16 [rows, >= heads * 128], rows contiguous")
-            if t.device != self.codes.device:
-                raise ValueError(f"k or v is on {t.device}, the cache on {self.codes.device}")
+            if t.device != self._device:
+                raise ValueError(f"k or v is on {t.device}, the cache on {self._device}")
             if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
                 raise ValueError("rows of k and v must be 16-byte aligned")
         if counts is not None:
@@ -264,11 +265,11 @@ class Int8KVCache:
         self._prepared(q.shape[0])
         if heads <= 0 or heads % self.heads:
             raise ValueError("heads must be a multiple of the cache's heads")
-        if q.device != self.codes.device:
-            raise ValueError(f"q is on {q.device}, the cache on {self.codes.device}")
+        if q.device != self._device:
+            raise ValueError(f"q is on {q.device}, the cache on {self._device}")
         cur = self._current()
         if out is None:
-            out = torch.empty((q.shape[0], heads * 128), dtype=torch.bfloat16, device=q.device)
+            out = torch.empty((q.shape[0], heads * 128), dtype=torch.bfloat16, device=self._device)
         if weights_out is None:
             weights_out = weights
         # a capture outlives these lengths: lay it out for any
@@ -279,7 +280,7 @@ class Int8KVCache:
             if len(self._work_bytes) >= 4096:
                 self._work_bytes.clear()
             need = self._work_bytes[sizes] = B.rbd_kv8_attn_workspace_bytes(self.sequences, self.heads, *sizes)
-        work = torch.empty((need,), dtype=torch.uint8, device=q.device) if need > 0 else None
+        work = torch.empty((need,), dtype=torch.uint8, device=self._device) if need > 0 else None
         B._kv8_attn(self._view, cur, self._lens_at, self._cu_at, q, out, heads, work, longest, causal, softmax_scale,
                     weights, weights_out)
         return out
@@ -289,7 +290,7 @@ class Int8KVCache:
         (zeros in front of a sequence's first)."""
         if tokens < 0:
             raise ValueError("tokens must not be negative")
-        k = torch.empty((self.sequences, tokens, self.heads * 128), dtype=torch.bfloat16, device=self.codes.device)
+        k = torch.empty((self.sequences, tokens, self.heads * 128), dtype=torch.bfloat16, device=self._device)
         v = torch.empty_like(k)
         B._kv8_read(self._view, self._current(), self._lens_at, k, v)
         return k, v
