@@ -190,3 +190,310 @@ def test_attend_keys_shared_by_many_blocks(fmt, causal, held, new, heads, group)
     fill(cache, plain, rng, held)
     w = torch.zeros((len(held), heads, 3200), device="cuda")
     check_attend(cache, plain, rng, new, heads * group, causal, q_gain=1.5, weights=w)
+
+
+def evict_case(rng, fmt, lens, heads, keep, recent, weights, in_place=False):
+    """Entry-level eviction of a filled cache against the plain one; returns nothing, asserts everything."""
+    n, width = len(lens), weights.shape[2]
+    per = -(-keep // PAGE)
+    total = sum(-(-x // PAGE) for x in lens) + n * per
+    cache = R.Int8KVCache(n, max(max(lens), keep, 1), heads, pages=total, code_format=fmt)
+    plain = PlainCache(n, heads, fmt)
+    fill(cache, plain, rng, lens)
+    dst = cache.spare_pages(n, per)
+    w = weights.cuda()
+    kept = torch.full((n, heads, keep), -7, dtype=torch.int32, device="cuda")
+    w_out = w if in_place else torch.full((n, heads, keep + 3), 9.0, device="cuda")
+    new_lens = torch.empty(n, dtype=torch.int32, device="cuda")
+    R.rbd_kv8_evict(w, cache.device_lens, cache.table, cache.codes, cache.scales, keep, recent, dst, kept, w_out, new_lens,
+                    fmt)
+    assert R.rbd_check() == 0
+    for b in range(n):
+        want = plain.evict(b, weights[b].numpy(), keep, recent)
+        m = min(lens[b], keep)
+        assert int(new_lens[b]) == m
+        for h in range(heads):
+            assert kept[b, h, :m].tolist() == want[h].tolist() and bool((kept[b, h, m:] == -1).all()), (b, h)
+            got = w_out[b, h].cpu()
+            assert torch.equal(got[:m].nan_to_num(-5.0), weights[b, h][torch.from_numpy(want[h])].nan_to_num(-5.0))
+            assert not got[m:].any()
+    # the kept tokens, read out of the new pages
+    cache.table[:, :per] = dst
+    cache.device_lens.copy_(new_lens)
+    cache._lens = [min(x, keep) for x in lens]
+    for b in range(n):
+        for h in range(heads):
+            for side in range(2):
+                got, s = code_values(cache, b, h, side, plain.len(b))
+                assert np.array_equal(s, plain.scales[b][h][side]) and np.array_equal(got, plain.codes[b][h][side])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lens,heads,keep,recent", [([1], 1, 1, 0), ([70, 3, 0], 2, 64, 10), ([200, 129], 3, 65, 65),
+                                                    ([500], 1, 100, 0), ([2000, 1000, 40], 2, 130, 7), ([64], 2, 64, 64),
+                                                    ([4100], 1, 4096, 100)])
+def test_evict(fmt, lens, heads, keep, recent):
+    rng = np.random.default_rng(keep + 13 * recent)
+    w = torch.from_numpy(np.exp(2 * rng.standard_normal((len(lens), heads, max(max(lens), keep)))).astype(np.float32))
+    evict_case(rng, fmt, lens, heads, keep, recent, w)
+
+
+def test_evict_ties_zeros_nan_negative_and_in_place():
+    rng = np.random.default_rng(5)
+    w = torch.zeros(3, 2, 700)
+    w[0, 0, ::3] = 1.0                                   # two values: ties everywhere
+    w[0, 1] = -0.0
+    w[0, 1, 5] = 0.0
+    w[1, 0] = torch.from_numpy(rng.integers(-3, 4, 700).astype(np.float32))
+    w[1, 1, 100:200] = float("nan")
+    w[1, 1, 300] = float("-inf")
+    w[2, 0, 50:60] = float("inf")
+    w[2, 1] = torch.from_numpy(np.float32(2.0) ** rng.integers(-149, 127, 700).astype(np.float32))
+    evict_case(rng, R.CODES_INT8, [700, 600, 500], 2, 150, 20, w)
+    evict_case(rng, R.CODES_E4M3, [700, 600, 500], 2, 450, 0, w)
+    evict_case(rng, R.CODES_INT8, [700, 600, 500], 2, 150, 20, w, in_place=True)
+
+
+def test_evict_longer_than_the_selection_holds_on_chip():
+    rng = np.random.default_rng(6)
+    n = 49152 + 3000                                     # the last 3000 positions are read from global memory
+    w = torch.from_numpy(rng.integers(0, 50, (1, 1, n)).astype(np.float32))
+    evict_case(rng, R.CODES_INT8, [n], 1, 700, 33, w)
+    evict_case(rng, R.CODES_INT8, [n], 1, 6000, 33, w, in_place=True)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_append_attend_evict_together(fmt):
+    """A serving loop: prompts, tokens one by one with weights, an eviction, more tokens; attention and the
+    cache's contents against the plain one throughout."""
+    rng = np.random.default_rng(8)
+    seqs, heads, group = 3, 2, 2
+    cache, plain = R.Int8KVCache(seqs, 400, heads, pages=24, code_format=fmt), PlainCache(seqs, heads, fmt)
+    w = torch.zeros((seqs, heads, 400), device="cuda")
+    pw = [np.zeros((heads, 400)) for _ in range(seqs)]
+    bound = [np.zeros((heads, 400)) for _ in range(seqs)]
+
+    def step(counts):
+        fill(cache, plain, rng, counts)
+        q = rand(rng, sum(counts), heads * group, 1.5)
+        y = cache.attend(dev(q), heads * group, weights=w).float().cpu().numpy().reshape(-1, heads * group, 128)
+        at = 0
+        for b, n in enumerate(counts):
+            o, dw, eo, ew = plain.attend(b, q[at:at + n].astype(np.float64), heads * group, True)
+            assert (np.abs(y[at:at + n] - o) <= eo).all()
+            held = plain.len(b)
+            pw[b][:, :held] += dw
+            bound[b][:, :held] += ew + 2.0 ** -23 * np.abs(pw[b][:, :held])
+            assert (np.abs(w[b, :, :held].double().cpu().numpy() - pw[b][:, :held]) <= bound[b][:, :held]).all()
+            at += n
+    step([150, 40, 301])
+    for _ in range(4):
+        step([1, 1, 1])
+    kept = cache.evict(w, 100, 30)
+    for b in range(seqs):
+        # which tokens stay is decided by the weights the kernels added up
+        got = kept[b].cpu().numpy()
+        m = min(plain.len(b), 100)
+        assert (got[:, m:] == -1).all()
+        for h in range(heads):
+            x, n = pw[b][h], plain.len(b)
+            out = np.setdiff1d(np.arange(n), got[h, :m])
+            assert out.size == n - m and (n <= 100 or (out < n - 30).all())
+            if out.size:
+                chosen = got[h, :m - 30]
+                assert x[chosen].min() >= x[out].max() - bound[b][h].max() * 2
+        forced = np.zeros((heads, plain.len(b)))
+        for h in range(heads):
+            forced[h, got[h, :m]] = 1.0
+            pw[b][h, :m], bound[b][h, :m] = pw[b][h, got[h, :m]], bound[b][h, got[h, :m]]
+            pw[b][h, m:], bound[b][h, m:] = 0.0, 0.0
+        plain.evict(b, forced, 100, 30)
+    check_codes(cache, plain)
+    assert cache.lens == [100, 44, 100] and cache.free_pages == 24 - 2 - 1 - 2
+    assert not w[:, :, 100:].any()
+    for _ in range(3):
+        step([1, 2, 0])
+    cache.release(1)
+    plain.codes[1] = [[np.zeros((0, 128), np.float32) for _ in range(2)] for _ in range(heads)]
+    plain.scales[1] = [[np.zeros(0, np.float32) for _ in range(2)] for _ in range(heads)]
+    w[1], pw[1][:], bound[1][:] = 0, 0, 0
+    step([0, 66, 1])
+    check_codes(cache, plain)
+    assert R.rbd_check() == 0
+
+
+def test_scales_far_apart_and_sharp_scores():
+    """Pages whose value scales differ by up to 2^80, with the small ones attended to; keys far larger in the last
+    pages, so that the running maximum moves; a query whose scores all vanish."""
+    rng = np.random.default_rng(9)
+    cache, plain = R.Int8KVCache(1, 512, 1), PlainCache(1, 1, 0)
+    for gain_k, gain_v in ((1.0, 2.0 ** 40), (1.0, 1.0), (6.0, 2.0 ** -40), (12.0, 2.0 ** -40), (0.0, 2.0 ** 20)):
+        k, v = rand(rng, 64, 1, gain_k, strong=False), rand(rng, 64, 1, gain_v, strong=False)
+        cache.append(dev(k), dev(v), [64])
+        plain.append(0, k, v)
+    for n in (1, 3, 70):
+        q = rand(rng, n, 1, 3.0)
+        q[0] = 0.0
+        q[n // 2] *= np.float32(2.0 ** -100)
+        check_attend(cache, plain, rng, [n], 1, False, q=q)
+        check_attend(cache, plain, rng, [n], 1, True, q=q)
+
+
+@pytest.mark.parametrize("n", [1, 12, 200])
+def test_a_nan_query_stays_in_its_row(n):
+    rng = np.random.default_rng(11)
+    cache, plain = R.Int8KVCache(1, 512, 1, code_format=R.CODES_E4M3), PlainCache(1, 1, 1)
+    cache.codes.fill_(0x7F)                              # pages that held something: E4M3 NaN behind the tokens
+    fill(cache, plain, rng, [300])
+    q = rand(rng, n, 2)
+    clean = check_attend(cache, plain, rng, [n], 2, True, q=q)
+    bad = q.copy()
+    bad[0, 1] = np.nan
+    bad[n - 1, 0, 3] = np.inf
+    got = cache.attend(dev(bad), 2).float().cpu().numpy().reshape(n, 2, 128)
+    assert np.isnan(got[0, 1]).all()
+    keep = np.ones((n, 2), bool)
+    keep[0, 1] = keep[n - 1, 0] = False
+    assert np.array_equal(got[keep], clean[keep])
+
+
+def test_device_side_metadata_is_refused_and_the_rest_is_right():
+    rng = np.random.default_rng(12)
+    for new in (1, 40, 300):
+        cache, plain = R.Int8KVCache(3, 512, 1), PlainCache(3, 1, 0)
+        fill(cache, plain, rng, [300, 310, 320])
+        q = rand(rng, 3 * new, 1)
+        cache.prepare([new] * 3, append=False)
+        want = cache.attend(dev(q), 1)
+        assert R.rbd_check() == 0
+        w = torch.zeros(3, 1, 512, device="cuda")
+        for spoil in ("page", "negative page", "length", "offsets"):
+            table, lens, cu = cache.table.clone(), cache.device_lens.clone(), cache._cu.clone()
+            if spoil == "page":
+                table[1, 2] = 10 ** 6
+            elif spoil == "negative page":
+                table[1, 0] = -1
+            elif spoil == "length":
+                lens[1] = 10 ** 6
+            else:
+                cu[3] = 10 ** 6
+            o = torch.zeros_like(want)
+            work = torch.empty(R.rbd_kv8_attn_workspace_bytes(3, 1, 1, 3 * new, 512, True), dtype=torch.uint8, device="cuda")
+            R.rbd_kv8_attn(dev(q), cu, lens, table, cache.codes, cache.scales, o, 1, work, 512, weights_in=w, weights_out=w)
+            assert R.rbd_check() == 1 and R.rbd_check() == 0
+            assert torch.equal(o[:new], want[:new])
+            if spoil != "offsets":
+                assert torch.equal(o[2 * new:], want[2 * new:])
+        before, scales = cache.codes.clone(), cache.scales.clone()
+        table = cache.table.clone()
+        table[1] = 10 ** 6
+        x = dev(rand(rng, 3 * new, 1))
+        R.rbd_kv8_append(x, x, cache._cu, cache.device_lens, table, cache.codes, cache.scales)
+        assert R.rbd_check() == 1
+        mine = cache.table[1].long()[:5]
+        assert torch.equal(cache.codes[mine], before[mine]) and torch.equal(cache.scales[mine], scales[mine])
+
+
+def test_rows_of_no_sequence_are_left_alone():
+    rng = np.random.default_rng(13)
+    cache, plain = R.Int8KVCache(2, 1024, 1), PlainCache(2, 1, 0)
+    fill(cache, plain, rng, [900, 100])
+    for a, b, tail in ((1, 1, 3), (30, 20, 30), (300, 5, 40)):
+        rows = 2 + a + b + tail
+        q, o = dev(rand(rng, rows, 2)), torch.full((rows, 256), 5.0, dtype=torch.bfloat16, device="cuda")
+        cu = torch.tensor([2, 2 + a, 2 + a + b], dtype=torch.int32, device="cuda")
+        work = torch.empty(R.rbd_kv8_attn_workspace_bytes(2, 1, 2, rows, 900), dtype=torch.uint8, device="cuda")
+        R.rbd_kv8_attn(q, cu, cache.device_lens, cache.table, cache.codes, cache.scales, o, 2, work if work.numel() else None,
+                       900)
+        assert R.rbd_check() == 0
+        assert bool((o[:2] == 5).all()) and bool((o[2 + a + b:] == 5).all()) and not bool((o[2:2 + a + b] == 5).all())
+
+
+def test_pool_beyond_32_bit_offsets():
+    """Pages in a pool of more than 2^31 bytes (and 2^32), the sequence's own ones at its end."""
+    rng = np.random.default_rng(14)
+    pages = (1 << 32) // 16384 + 40
+    cache, plain = R.Int8KVCache(1, 1024, 1, pages=pages), PlainCache(1, 1, 0)
+    cache._free = list(range(pages - 20, pages))         # taken from the far end
+    fill(cache, plain, rng, [500])
+    assert int(cache.table[0, 0]) > (1 << 32) // 16384
+    check_codes(cache, plain)
+    w = torch.zeros(1, 1, 1024, device="cuda")
+    check_attend(cache, plain, rng, [1], 2, True, weights=w)
+    check_attend(cache, plain, rng, [300], 2, True, weights=w)
+    k, v = cache.tail(500)
+    assert torch.equal(v[0].cpu(), torch.from_numpy(plain.values(0, 0, 1)).bfloat16())
+
+
+@pytest.mark.parametrize("counts", [[1, 1, 1], [20, 20, 20], [90, 90, 90]])
+def test_captured_steps_replay_with_other_lengths(counts):
+    """Append and attend captured once (two graphs, with and without weights), replayed at other lengths and
+    inputs in turn: the results are those of eager calls on an equal cache."""
+    rng = np.random.default_rng(15)
+    heads, group, rows = 2, 2, sum(counts)
+    caches = [R.Int8KVCache(3, 700, heads) for _ in range(2)]
+    k0, v0 = rand(rng, 330, heads), rand(rng, 330, heads)
+    for c in caches:
+        c.append(dev(k0), dev(v0), [100, 30, 200])
+    kb, vb = (torch.empty((rows, heads * 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qb = torch.empty((rows, heads * group * 128), dtype=torch.bfloat16, device="cuda")
+    outs = [torch.empty_like(qb) for _ in range(2)]
+    w = torch.zeros(3, heads, 700, device="cuda")
+    we = torch.zeros_like(w)
+    live, eager = caches
+    graphs = []
+    side = torch.cuda.Stream()
+    for i in range(2):
+        if i == 0:
+            live.prepare(counts)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            live.append(kb, vb)
+            live.attend(qb, heads * group, out=outs[i], weights=w if i else None)
+        graphs.append(g)
+    for step in range(4):
+        k, v, q = rand(rng, rows, heads), rand(rng, rows, heads), rand(rng, rows, heads * group)
+        if step:
+            live.prepare(counts)
+        kb.copy_(dev(k)), vb.copy_(dev(v)), qb.copy_(dev(q))
+        graphs[step % 2].replay()
+        eager.append(dev(k), dev(v), counts)
+        y = eager.attend(dev(q), heads * group, weights=we if step % 2 else None)
+        torch.cuda.synchronize()
+        assert R.rbd_check() == 0
+        # (the splits of a long layout join in another order: a bf16 step at most, from float32 sums)
+        d = (outs[step % 2].float() - y.float()).abs()
+        assert bool((d <= 2.0 ** -7 * y.float().abs() + 1e-5).all())
+        assert torch.allclose(w, we, rtol=1e-5, atol=1e-6)
+    for a, b in zip(live.tail(400), eager.tail(400)):
+        assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    rng = np.random.default_rng(16)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    for s in streams:
+        cache, plain = R.Int8KVCache(2, 3000, 2), PlainCache(2, 2, 0)
+        with torch.cuda.stream(s):
+            fill(cache, plain, rng, [2500, 700])
+        runs.append((cache, [dev(rand(rng, 2, 8)), dev(rand(rng, 600, 8))]))
+    torch.cuda.synchronize()
+    want = []
+    for cache, qs in runs:
+        for q in qs:
+            cache.prepare([q.shape[0] // 2] * 2, append=False)
+            want.append(cache.attend(q, 8))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for i in range(2):
+            for s, (cache, qs) in zip(streams, runs):
+                with torch.cuda.stream(s):
+                    cache.prepare([qs[i].shape[0] // 2] * 2, append=False)
+                    got.append((s, cache.attend(qs[i], 8)))
+        torch.cuda.synchronize()
+        assert R.rbd_check() == 0
+        for (_, y), x in zip(got, [want[0], want[2], want[1], want[3]]):
+            assert torch.equal(y, x)
