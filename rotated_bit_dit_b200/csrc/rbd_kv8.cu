@@ -64,21 +64,16 @@ __global__ void __launch_bounds__(256)
                       const uint16_t* __restrict__ k, int64_t ldk, const uint16_t* __restrict__ v, int64_t ldv,
                       int rows) {
   __shared__ uint32_t red[2][4];
-  auto pages_of = [&](int b) {
-    int r0, n;
-    if (!kv8_rows(cu, b, rows, r0, n) || n == 0) return 0;
-    const int len = __ldg(lens + b);
+  auto pages_of = [&](int n, int len) {
     if (len < 0 || (int64_t)len + n > (int64_t)c.max_pages * kKv8Page) {
       record_refusal();
       return 0;
     }
     return (len + n - 1) / kKv8Page - len / kKv8Page + 1;
   };
-  int b, idx;
-  if (!kv8_find(c.seqs, blockIdx.x / c.heads, pages_of, b, idx)) return;
-  const int head = blockIdx.x % c.heads;
-  const int len = __ldg(lens + b);
-  const int r0 = __ldg(cu + b), n = __ldg(cu + b + 1) - r0;
+  Kv8Item it;
+  if (!kv8_find(cu, lens, c.seqs, rows, blockIdx.x / c.heads, pages_of, it)) return;
+  const int head = blockIdx.x % c.heads, b = it.b, idx = it.idx, len = it.len, r0 = it.r0, n = it.n;
   const int p = len / kKv8Page + idx;
   const int held = max(0, len - p * kKv8Page);                       // rows that already hold tokens
   const int end = min(kKv8Page, len + n - p * kKv8Page);             // rows held afterwards

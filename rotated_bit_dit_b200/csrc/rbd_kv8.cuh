@@ -85,15 +85,26 @@ __device__ __forceinline__ bool kv8_rows(const int32_t* cu, int b, int rows, int
   return false;
 }
 
-// Which sequence item x belongs to, when sequence b has count(b) items in a row:
-// b and the item's index inside it.  Every warp of the block finds out by itself
-// (32 sequences per step, an inclusive scan of their counts); all 32 lanes call.
+// What a block works on: sequence b, the item's index among the sequence's, and the
+// sequence's rows of the packed tensors and length.
+struct Kv8Item {
+  int b, idx, r0, n, len;
+};
+
+// The item x of a launch, when sequence b has count(n, len) items in a row.  Every warp of the block finds out by
+// itself (32 sequences per step, an inclusive scan of their counts; what the lanes have read is passed on, not read
+// again); all 32 lanes call.  A sequence whose rows lie outside the packed tensors (recorded) has none.
 template <class Count>
-__device__ __forceinline__ bool kv8_find(int seqs, int x, Count count, int& b, int& idx) {
+__device__ __forceinline__ bool kv8_find(const int32_t* cu, const int32_t* lens, int seqs, int rows, int x, Count count,
+                                         Kv8Item& it) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   for (int b0 = 0; b0 < seqs; b0 += 32) {
-    int c = b0 + lane < seqs ? count(b0 + lane) : 0;
+    int r0 = 0, n = 0, len = 0, c = 0;
+    if (b0 + lane < seqs) {
+      len = __ldg(lens + b0 + lane);
+      if (kv8_rows(cu, b0 + lane, rows, r0, n) && n > 0) c = count(n, len);
+    }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, c, off);
@@ -103,8 +114,11 @@ __device__ __forceinline__ bool kv8_find(int seqs, int x, Count count, int& b, i
     if (hit) {
       const int l = __ffs(hit) - 1;
       const int before = __shfl_sync(0xffffffffu, c, l > 0 ? l - 1 : 0);
-      b = b0 + l;
-      idx = x - base - (l > 0 ? before : 0);
+      it.b = b0 + l;
+      it.idx = x - base - (l > 0 ? before : 0);
+      it.r0 = __shfl_sync(0xffffffffu, r0, l);
+      it.n = __shfl_sync(0xffffffffu, n, l);
+      it.len = __shfl_sync(0xffffffffu, len, l);
       return true;
     }
     base += __shfl_sync(0xffffffffu, c, 31);

@@ -70,12 +70,14 @@ __device__ __forceinline__ void kv8_row_scale(uint32_t amax, float& f, float& in
   inv = __uint_as_float((uint32_t)(254 - field) << 23);
 }
 
-// Length of sequence b, or 0 (recorded) when it exceeds what the call declared.
-__device__ __forceinline__ int kv8_len(const Kv8View& c, const Kv8AttnArgs& a, int b) {
-  const int len = __ldg(a.lens + b);
+// A sequence's length, or 0 (recorded) when it exceeds what the call declared.
+__device__ __forceinline__ int kv8_length(const Kv8View& c, const Kv8AttnArgs& a, int len) {
   if (len >= 0 && len <= a.max_len && len <= c.max_pages * kKv8Page) return len;
   record_refusal();
   return 0;
+}
+__device__ __forceinline__ int kv8_len(const Kv8View& c, const Kv8AttnArgs& a, int b) {
+  return kv8_length(c, a, __ldg(a.lens + b));
 }
 
 // Keys query token i of n sees.
@@ -162,16 +164,12 @@ __global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kerne
   const int g = lane >> 2, l = lane & 3;
   const int head = blockIdx.y, split = blockIdx.z;
 
-  auto tiles_of = [&](int b) {
-    int r0, n;
-    kv8_rows(a.cu, b, a.rows, r0, n);
-    return (int)(((int64_t)n * a.group + ROWS - 1) / ROWS);
-  };
-  int b, tile;
-  if (!kv8_find(c.seqs, blockIdx.x, tiles_of, b, tile)) return;
-  int r0, n;
-  kv8_rows(a.cu, b, a.rows, r0, n);
-  const int len = kv8_len(c, a, b);
+  Kv8Item it;
+  if (!kv8_find(a.cu, a.lens, c.seqs, a.rows, blockIdx.x,
+                [&](int n, int) { return (int)(((int64_t)n * a.group + ROWS - 1) / ROWS); }, it))
+    return;
+  const int b = it.b, tile = it.idx, r0 = it.r0, n = it.n;
+  const int len = kv8_length(c, a, it.len);
   const int row_first = tile * ROWS;
   const int nrows = min(ROWS, n * a.group - row_first);
   const int vis = min(len, kv8_visible(a.causal, len, n, (row_first + nrows - 1) / a.group));
@@ -181,6 +179,20 @@ __global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kerne
   const int p1 = min(p0 + per, (vis + kKv8Page - 1) / kKv8Page);
   const int cnt = p1 - p0 > warp ? (p1 - p0 - warp + W - 1) / W : 0;
 
+  // The loads a block starts with depend on one another (offsets, page, codes): what does not is asked for first.
+  uint4 qw[NQ][4];                                     // row g of every 8, channels 32 l .. 32 l + 31
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const int r = row_first + 8 * q + g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) qw[q][i] = make_uint4(0u, 0u, 0u, 0u);
+    if (8 * q + g < nrows) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(r0 + r / a.group) * a.ldq +
+                                                        (int64_t)(head * a.group + r % a.group) * kKv8Dim + 32 * l);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qw[q][i] = __ldg(src + i);
+    }
+  }
   uint64_t* full = bars + 2 * warp;                                  // keys, values
   if (lane == 0) {
     mbar_init(&full[0], 1);
@@ -192,16 +204,13 @@ __global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kerne
   // 32 of the warp's pages at a time: lane i knows page i, its scales, log2 s_v and 1 / s_v
   int my_page = -1;
   float my_sk = 1.f, my_lsv = 0.f, my_inv = 1.f;
-  auto look_up = [&](int i0) {
-    my_page = -1;
-    if (i0 + lane < cnt) {
-      my_page = kv8_page(c, b, p0 + warp + (i0 + lane) * W);
-      if (my_page >= 0) {
-        const float2 sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, my_page, head, 0));
-        my_sk = sc.x;
-        my_lsv = log2f(sc.y);
-        my_inv = 1.0f / sc.y;
-      }
+  auto look_up = [&](int i0) { my_page = i0 + lane < cnt ? kv8_page(c, b, p0 + warp + (i0 + lane) * W) : -1; };
+  auto look_up_scales = [&]() {
+    if (my_page >= 0) {
+      const float2 sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, my_page, head, 0));
+      my_sk = sc.x;
+      my_lsv = log2f(sc.y);
+      my_inv = 1.0f / sc.y;
     }
   };
   auto issue = [&](int side, int page) {       // an index outside the pool: the buffer's old contents, skipped below
@@ -219,24 +228,15 @@ __global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kerne
     issue(0, page);
     issue(1, page);
   }
+  look_up_scales();
 
-  // query fragments: row g of every 8, channels 32 l .. 32 l + 31
+  // query fragments
   uint32_t qb[NQ][8][2];
   float coef[NQ][2];                                   // of rows 2 l and 2 l + 1 of every 8
   int lim[NQ][2];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
-    const int r = row_first + 8 * q + g;
-    uint4 w[4];
-    if (8 * q + g < nrows) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(r0 + r / a.group) * a.ldq +
-                                                        (int64_t)(head * a.group + r % a.group) * kKv8Dim + 32 * l);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __ldg(src + i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
+    const uint4 (&w)[4] = qw[q];
     uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -285,7 +285,10 @@ __global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kerne
   for (int i = 0; i < cnt; ++i) {
     const float sk = __shfl_sync(0xffffffffu, my_sk, i & 31), lsv = __shfl_sync(0xffffffffu, my_lsv, i & 31);
     const float inv_sv = __shfl_sync(0xffffffffu, my_inv, i & 31);
-    if (((i + 1) & 31) == 0) look_up(i + 1);
+    if (((i + 1) & 31) == 0) {
+      look_up(i + 1);
+      look_up_scales();
+    }
     const int next = __shfl_sync(0xffffffffu, my_page, (i + 1) & 31);
     const bool more = i + 1 < cnt;
     if (!__all_sync(0xffffffffu, mbar_wait(&full[0], i & 1))) { ok = false; break; }

@@ -127,6 +127,14 @@ __device__ __forceinline__ void tc_commit_if(uint32_t leader, uint64_t* bar) {
       "r"(leader)
       : "memory");
 }
+// Items (256 rows) of a sequence with n query tokens.
+struct Kv8TileItems {
+  int group;
+  __device__ int operator()(int n, int) const {
+    return (int)(((int64_t)n * group + 2 * kTlRows - 1) / (2 * kTlRows));
+  }
+};
+
 constexpr uint32_t kIdescBMn = 1u << 16;           // B is MN-major
 
 template <int N>
@@ -220,16 +228,10 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
   // items of a launch run from the last to the first: with a causal mask the later rows of a sequence see the
   // most keys, and long blocks had better start early
   const int item = a.items - 1 - (int)blockIdx.x;
-  auto tiles_of = [&](int b) {
-    int r0, n;
-    kv8_rows(a.cu, b, a.rows, r0, n);
-    return (int)(((int64_t)n * a.group + 2 * kTlRows - 1) / (2 * kTlRows));
-  };
-  int b, tile;
-  if (!kv8_find(c.seqs, item, tiles_of, b, tile)) return;
-  int r0, n;
-  kv8_rows(a.cu, b, a.rows, r0, n);
-  const int len = kv8_len(c, a, b);
+  Kv8Item it;
+  if (!kv8_find(a.cu, a.lens, c.seqs, a.rows, item, Kv8TileItems{a.group}, it)) return;
+  const int b = it.b, tile = it.idx, r0 = it.r0, n = it.n;
+  const int len = kv8_length(c, a, it.len);
   const int row_first = tile * 2 * kTlRows;
   const int nrows = min(2 * kTlRows, n * a.group - row_first);
   // 128-key steps of either query tile, and the ones of this split
@@ -655,16 +657,10 @@ constexpr uint32_t kWgSmem = kWgBar + 256 + 1024;
 
 // The rows' constants c = -(m + log2 L) and numbers of keys seen, beside their factors: [heads][items][2][3][128].
 __global__ void __launch_bounds__(2 * kTlRows) kv8_rows_kernel(const Kv8View c, const Kv8AttnArgs a) {
-  auto tiles_of = [&](int b) {
-    int r0, n;
-    kv8_rows(a.cu, b, a.rows, r0, n);
-    return (int)(((int64_t)n * a.group + 2 * kTlRows - 1) / (2 * kTlRows));
-  };
-  int b, tile;
-  if (!kv8_find(c.seqs, blockIdx.x, tiles_of, b, tile)) return;
-  int r0, n;
-  kv8_rows(a.cu, b, a.rows, r0, n);
-  const int len = kv8_len(c, a, b);
+  Kv8Item it;
+  if (!kv8_find(a.cu, a.lens, c.seqs, a.rows, blockIdx.x, Kv8TileItems{a.group}, it)) return;
+  const int tile = it.idx, r0 = it.r0, n = it.n;
+  const int len = kv8_length(c, a, it.len);
   const int head = blockIdx.y;
   const int rr = tile * 2 * kTlRows + threadIdx.x;
   float k = -INFINITY;                          // no such row, or one without keys: 2^(-inf) = 0
@@ -711,7 +707,7 @@ __global__ void __launch_bounds__(kWgThreads, 2)
   for (int i = lane; i < b; i += 32) {
     int x0, xn;
     kv8_rows(a.cu, i, a.rows, x0, xn);
-    item0 += (int)(((int64_t)xn * a.group + 2 * kTlRows - 1) / (2 * kTlRows));
+    item0 += Kv8TileItems{a.group}(xn, 0);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) item0 += __shfl_xor_sync(0xffffffffu, item0, off);
