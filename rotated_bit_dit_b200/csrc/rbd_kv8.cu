@@ -23,16 +23,18 @@ namespace {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-// Largest finite |bf16| bit pattern of a word's two values, max'ed into m (an infinity or NaN counts as zero).
-__device__ __forceinline__ uint32_t finite_amax(uint32_t m, uint32_t w) {
-  const uint32_t a = w & 0x7FFFu, b = (w >> 16) & 0x7FFFu;
-  return max(m, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
+// The larger |bf16| bit patterns of a word's two halves and m's, half by half.
+__device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
+// The same with infinities and NaN counted as zero.
+__device__ __forceinline__ uint32_t finite_amax2(uint32_t m, uint32_t w) {
+  const uint32_t a = w & 0x7FFF7FFFu;
+  return __vmaxu2(m, ((a & 0xFFFFu) < 0x7F80u ? a & 0xFFFFu : 0u) | ((a >> 16) < 0x7F80u ? a & 0xFFFF0000u : 0u));
 }
 
-template <int FMT>
+template <int FMT, bool RAW>
 __device__ __forceinline__ uint32_t encode_bf16x4(uint32_t w0, uint32_t w1, float inv) {
   const float x[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)};
-  return kv8_encode4<FMT, true>(x, inv);
+  return kv8_encode4<FMT, RAW>(x, inv);
 }
 
 // Codes of four stored codes under a new scale: the values they stand for, quantised again.
@@ -59,7 +61,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // Heads are the fastest index of the blocks: those that run together then read whole
 // rows of k and v, not 256 bytes of each.
 template <int FMT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     kv8_append_kernel(const Kv8View c, const int32_t* __restrict__ lens, const int32_t* __restrict__ cu,
                       const uint16_t* __restrict__ k, int64_t ldk, const uint16_t* __restrict__ v, int64_t ldv,
                       int rows) {
@@ -91,16 +93,30 @@ __global__ void __launch_bounds__(256)
     raw[i] = make_uint4(0u, 0u, 0u, 0u);
     if (t >= held && t < end)
       raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (first + t) * ld + head * kKv8Dim + 8 * chunk8));
-    m = finite_amax(finite_amax(finite_amax(finite_amax(m, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
+    m = amax2(amax2(amax2(amax2(m, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
   }
   const int page = kv8_page(c, b, p);            // (after the loads above: none waits for it)
   if (page < 0) return;
   float* scale = c.scales + kv8_scale(c, page, head, side);
   const float s_old = held > 0 ? *scale : kKv8Floor;
-  m = __reduce_max_sync(0xffffffffu, m);
-  if ((tid & 31) == 0) red[side][tid >> 5] = m;
-  __syncthreads();
-  m = max(max(red[side][0], red[side][1]), max(red[side][2], red[side][3]));
+  auto block_max = [&](uint32_t v) {            // of either side, into red
+    v = __reduce_max_sync(0xffffffffu, max(v & 0xFFFFu, v >> 16));
+    if ((tid & 31) == 0) red[side][tid >> 5] = v;
+    __syncthreads();
+  };
+  auto side_max = [&](int sd) { return max(max(red[sd][0], red[sd][1]), max(red[sd][2], red[sd][3])); };
+  block_max(m);
+  m = side_max(side);
+  const bool clean = max(m, side_max(side ^ 1)) < 0x7F80u;
+  if (!clean) {                                 // an infinity or NaN among the block's values: again, without them
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      m = finite_amax2(finite_amax2(finite_amax2(finite_amax2(m, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
+    __syncthreads();
+    block_max(m);
+    m = side_max(side);
+  }
   const float amax = __uint_as_float(m << 16);
   const float s = fmaxf(fmaxf(s_old, __fmul_rn(amax, kv8_inv_qmax<FMT>())), kKv8Floor);
   const float inv = __frcp_rn(s);
@@ -110,7 +126,10 @@ __global__ void __launch_bounds__(256)
     const int t = row0 + 8 * i;
     uint2* dst = reinterpret_cast<uint2*>(tile + kv8_chunk(t, chunk8 >> 1) + 8 * (chunk8 & 1));
     if (t >= held && t < end) {
-      *dst = make_uint2(encode_bf16x4<FMT>(raw[i].x, raw[i].y, inv), encode_bf16x4<FMT>(raw[i].z, raw[i].w, inv));
+      *dst = clean ? make_uint2(encode_bf16x4<FMT, false>(raw[i].x, raw[i].y, inv),
+                                encode_bf16x4<FMT, false>(raw[i].z, raw[i].w, inv))
+                   : make_uint2(encode_bf16x4<FMT, true>(raw[i].x, raw[i].y, inv),
+                                encode_bf16x4<FMT, true>(raw[i].z, raw[i].w, inv));
     } else if (t < held && s > s_old) {
       const uint2 w = *dst;
       *dst = make_uint2(requantise4<FMT>(w.x, s_old, inv), requantise4<FMT>(w.y, s_old, inv));

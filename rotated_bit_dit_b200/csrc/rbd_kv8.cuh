@@ -131,9 +131,10 @@ __host__ __device__ __forceinline__ constexpr float kv8_inv_qmax() {
   return FMT == RBD_CODES_INT8 ? 1.f / 127.f : 1.f / 448.f;
 }
 
-// Code bytes of four values x under the inverse scale inv.  RAW: the values come from a caller, whose NaN is stored
-// as zero (an infinity becomes the largest code).  INT8 rounds by adding 1.5 * 2^23, whose low byte is then the
-// two's complement code (the conversion instruction runs at an eighth of the rate).
+// Code bytes of four values x under the inverse scale inv.  RAW: infinities and NaN may be among them (stored as the
+// largest code and as zero); without, |x| is at most the scale's own qmax s (1 + 2^-22), which rounds to the largest
+// code by itself.  INT8 rounds by adding 1.5 * 2^23, whose low byte is then the two's complement code (the conversion
+// instruction runs at an eighth of the rate).
 template <int FMT, bool RAW>
 __device__ __forceinline__ uint32_t kv8_encode4(const float (&x)[4], float inv) {
   float y[4];
@@ -141,11 +142,12 @@ __device__ __forceinline__ uint32_t kv8_encode4(const float (&x)[4], float inv) 
   for (int j = 0; j < 4; ++j) {
     y[j] = __fmul_rn(x[j], inv);
     if (RAW) y[j] = y[j] == y[j] ? y[j] : 0.f;
+    if (RAW && FMT == RBD_CODES_INT8) y[j] = fminf(fmaxf(y[j], -127.f), 127.f);
   }
   if (FMT == RBD_CODES_INT8) {
     uint32_t u[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(__fadd_rn(fminf(fmaxf(y[j], -127.f), 127.f), 12582912.f));
+    for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(__fadd_rn(y[j], 12582912.f));
     return prmt(prmt(u[0], u[1], 0x0040u), prmt(u[2], u[3], 0x0040u), 0x5410u);
   }
   uint32_t d;

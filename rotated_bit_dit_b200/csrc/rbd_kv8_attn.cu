@@ -121,7 +121,7 @@ constexpr int kStORow = kKv8Dim + 4;                                 // padded r
 
 template <int NQ>
 struct StreamShape {
-  static constexpr int kWarps = 12;
+  static constexpr int kWarps = NQ == 1 ? 12 : 8;                    // (of 8, registers for 16 rows: 12 spill, 54 us against 51)
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NQ;
   static constexpr uint32_t kRing = kWarps * kStPage;
