@@ -501,7 +501,10 @@ int64_t rbd_kv8_attn_workspace_bytes(int64_t seqs, int64_t heads, int64_t q_head
  *           b * w_seq + h * w_head + t, w_head >= max_len: weights_out = weights_in +
  *           the sum, over the queries of sequence b and the query heads of cache
  *           head h, of the weight key t got; t < lens[b] only.  They may be the same.
- *   work    rbd_kv8_attn_workspace_bytes(...) bytes, 256-byte aligned (NULL if 0).
+ *   work    rbd_kv8_attn_workspace_bytes(...) bytes, 256-byte aligned (NULL if 0):
+ *           float32 partial results where keys are split; with weights and few rows
+ *           a sequence 4 bytes per (row, query head, key up to max_len); with many
+ *           rows operand images of the keys and values, 2 GiB at most.
  * Scores, softmax statistics and sums are float32 on exact products of codes and
  * queries; the softmax's numerators are rounded to fp16 for the second product.
  * No result depends on timing.  rows * q_heads <= 2^30.                       */

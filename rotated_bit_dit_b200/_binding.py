@@ -434,7 +434,7 @@ def _bf16_rows(t: torch.Tensor, cols: int, what: str) -> int:
     s = t.shape
     if t.dtype != torch.bfloat16 or len(s) != 2 or s[1] < cols or t.stride(1) != 1:
         raise ValueError(f"{what} must be bf16 [rows, >= {cols}], rows contiguous")
-    return t.stride(0) if s[0] > 1 else max(t.stride(0), cols + -cols % 8)
+    return t.stride(0) if s[0] > 1 else cols + -cols % 8       # a single row's stride means nothing
 
 
 def _weights(t: torch.Tensor, seqs: int, heads: int, what: str):

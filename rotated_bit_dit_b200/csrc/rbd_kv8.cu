@@ -348,37 +348,46 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const Kv8View c
 template <int FMT>
 __global__ void __launch_bounds__(256, 4)
     kv8_gather_kernel(const Kv8View c, const int32_t* __restrict__ dst_table, int64_t ld_dst,
-                      const int32_t* __restrict__ kept, const int32_t* __restrict__ lens_out, int keep) {
+                      const int32_t* __restrict__ kept, int keep) {
   __shared__ uint32_t red[2][4];
+  __shared__ int64_t row_at[kKv8Page];          // byte of the kept token's row of keys, -1 without a token, -2 without a page
+  __shared__ float2 row_scale[kKv8Page];
   const int b = blockIdx.z, head = blockIdx.y, p = blockIdx.x;
-  const int m = min(__ldg(lens_out + b), keep);
-  const int end = min(kKv8Page, m - p * kKv8Page);
-  if (end <= 0) return;
   const int dst_page = __ldg(dst_table + b * ld_dst + p);
+  // (kept is -1 behind the last token: how many there are need not be waited for)
+  if (threadIdx.x < kKv8Page) {
+    const int j = p * kKv8Page + threadIdx.x;
+    const int src = j < keep ? __ldg(kept + ((int64_t)b * c.heads + head) * keep + j) : -1;
+    int64_t at = -1;
+    float2 sc = make_float2(0.f, 0.f);
+    if (src >= 0) {
+      const int page = kv8_page(c, b, src / kKv8Page);
+      at = page >= 0 ? kv8_tile(c, page, head, 0) + src % kKv8Page * kKv8Dim : -2;
+      if (page >= 0) sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page, head, 0));
+    }
+    row_at[threadIdx.x] = at;
+    row_scale[threadIdx.x] = sc;
+  }
+  __syncthreads();
+  if (row_at[0] == -1) return;
   if (dst_page < 0 || dst_page >= c.pages) {
     if (threadIdx.x == 0) record_refusal();
     return;
   }
   const int side = threadIdx.x >> 7, tid = threadIdx.x & 127;
   const int chunk = tid & 7, row0 = tid >> 3;
-  const int32_t* from = kept + ((int64_t)b * c.heads + head) * keep + p * kKv8Page;
   uint4 raw[4];
   float s_src[4];
   float am = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = row0 + 16 * i;
+    const int64_t at = row_at[row0 + 16 * i];
     raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    s_src[i] = 0.f;
-    if (t < end) {
-      const int src = __ldg(from + t);
-      const int page = kv8_page(c, b, src / kKv8Page);
-      if (page >= 0) {
-        raw[i] = *reinterpret_cast<const uint4*>(c.codes + kv8_tile(c, page, head, side) +
-                                                 kv8_chunk(src % kKv8Page, chunk));
-        s_src[i] = c.scales[kv8_scale(c, page, head, side)];
-      }
-    }
+    // (a row's chunks are permuted by its token's last three bits, which are the row address's bits 7 to 9)
+    if (at >= 0)
+      raw[i] = *reinterpret_cast<const uint4*>(c.codes + at + side * kKv8Side + ((chunk ^ ((int)(at >> 7) & 7)) << 4));
+    const float2 sc = row_scale[row0 + 16 * i];
+    s_src[i] = side ? sc.y : sc.x;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(256, 4)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = row0 + 16 * i;
-    if (t < end)
+    if (row_at[t] != -1)
       *reinterpret_cast<uint4*>(tile + kv8_chunk(t, chunk)) =
           make_uint4(requantise4<FMT>(raw[i].x, s_src[i], inv), requantise4<FMT>(raw[i].y, s_src[i], inv),
                      requantise4<FMT>(raw[i].z, s_src[i], inv), requantise4<FMT>(raw[i].w, s_src[i], inv));
@@ -458,8 +467,8 @@ cudaError_t launch_kv8_evict(const Kv8View& c, bool e4m3, const float* weights, 
   if (e != cudaSuccess) return e;
   kv8_select_kernel<<<dim3(c.heads, c.seqs), kSelThreads, smem, st>>>(c, a, cap);
   const dim3 grid((keep + kKv8Page - 1) / kKv8Page, c.heads, c.seqs);
-  if (e4m3) kv8_gather_kernel<RBD_CODES_E4M3><<<grid, 256, 0, st>>>(c, dst_table, ld_dst, kept, lens_out, keep);
-  else kv8_gather_kernel<RBD_CODES_INT8><<<grid, 256, 0, st>>>(c, dst_table, ld_dst, kept, lens_out, keep);
+  if (e4m3) kv8_gather_kernel<RBD_CODES_E4M3><<<grid, 256, 0, st>>>(c, dst_table, ld_dst, kept, keep);
+  else kv8_gather_kernel<RBD_CODES_INT8><<<grid, 256, 0, st>>>(c, dst_table, ld_dst, kept, keep);
   return cudaGetLastError();
 }
 

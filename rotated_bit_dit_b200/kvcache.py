@@ -246,6 +246,7 @@ class Int8KVCache:
                 raise ValueError(f"k or v is on {t.device}, the cache on {self._device}")
             if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
                 raise ValueError("rows of k and v must be 16-byte aligned")
+        cur = self._current()
         if counts is not None:
             if k.shape[0] != sum(int(c) for c in counts) or v.shape[0] != k.shape[0]:
                 raise ValueError("counts and rows differ")
@@ -253,7 +254,7 @@ class Int8KVCache:
         self._prepared(k.shape[0])
         if not self._may_append:
             raise ValueError("prepared without append")
-        B._kv8_append(self._view, self._current(), self._before_at, self._cu_at, k, v)
+        B._kv8_append(self._view, cur, self._before_at, self._cu_at, k, v)
 
     def attend(self, q: torch.Tensor, heads: int, causal: bool = True, out: Optional[torch.Tensor] = None,
                softmax_scale: float = 128 ** -0.5, weights: Optional[torch.Tensor] = None,
@@ -319,7 +320,15 @@ class Int8KVCache:
         if sequences * pages > len(self._free):
             raise ValueError(f"{sequences * pages} pages needed, {len(self._free)} free")
         taken = [self._free.pop() for _ in range(sequences * pages)]
-        return torch.tensor(taken, dtype=torch.int32).view(sequences, pages).to(self.codes.device)
+        return torch.tensor(taken, dtype=torch.int32).view(sequences, pages).to(self._device)
+
+    def give_back(self, pages: torch.Tensor) -> None:
+        """Return pages that spare_pages() took to the pool (waits for the device)."""
+        back = pages.flatten().tolist()
+        held = set(self._free).union(*self._pages)
+        if len(set(back)) != len(back) or any(not 0 <= p < self.codes.shape[0] or p in held for p in back):
+            raise ValueError("pages that were not taken")
+        self._free += reversed(back)
 
     def evict(self, weights: torch.Tensor, keep: int, recent: int) -> torch.Tensor:
         """Cut every sequence to at most `keep` tokens, per head: its last `recent` tokens and those of largest

@@ -169,6 +169,12 @@ def test_bookkeeping(launches):
     assert c.lens == [0, 51, 57] and check_books(c, 12) and c.free_pages == 10
     taken = c.spare_pages(2, 3)
     assert taken.shape == (2, 3) and c.free_pages == 4 and not check_books(c, 12)
+    for bad in (torch.tensor([c._free[0]]), torch.tensor([c._pages[1][0]]), torch.tensor([12]), torch.tensor([-1]),
+                torch.cat([taken[0], taken[0]])):
+        with pytest.raises(ValueError):
+            c.give_back(bad)
+    c.give_back(taken)
+    assert c.free_pages == 10 and check_books(c, 12)
 
 
 def test_refused_calls_change_nothing(launches):
@@ -211,7 +217,7 @@ def test_binding_refuses_shapes_and_devices():
         with pytest.raises(ValueError):                  # the last one: not on a GPU
             B._kv8(**a)
     q = torch.zeros(4, 256, dtype=torch.bfloat16)
-    assert B._bf16_rows(q, 256, "q") == 256 and B._bf16_rows(q[:1, :200], 130, "q") == 256
+    assert B._bf16_rows(q, 256, "q") == 256 and B._bf16_rows(q[:1, :200], 130, "q") == 136
     for bad in (q.float(), q[0], q.t(), q[:, :100]):
         with pytest.raises(ValueError):
             B._bf16_rows(bad, 256, "q")
