@@ -218,9 +218,9 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
   uint64_t* v_empty = bars + 6;     // [2]
   uint64_t* s_full = bars + 8;      // [2] per query tile, commit
   uint64_t* p_full = bars + 10;     // [2] per query tile, 4 softmax warps
-  uint64_t* q_full = bars + 12;     // 8 softmax warps
-  uint64_t* o_done = bars + 13;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 14);
+  uint64_t* q_full = bars + 12;     // [2] per query tile, 4 softmax warps
+  uint64_t* o_done = bars + 14;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 15);
   float* coef = reinterpret_cast<float*>(smem + kTlCoef);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&q_full[i], 4);
     }
-    mbar_init(q_full, 8);
     mbar_init(o_done, 1);
     fence_barrier_init();
   }
@@ -352,13 +352,16 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
       };
       // A wait costs about 100 cycles even when there is nothing to wait for, and the tensor core's queue is short:
       // every wait stands behind eight products that are still running.
-      bool ok = wait_warp(q_full, 0) && wait_warp(&k_full[0], 0);
+      bool ok = wait_warp(&k_full[0], 0);
       if (ok) {
-        tc_fence_after();
-        for (int t = 0; t < 2; ++t)
-          if (cnt_t[t] > 0) issue_qk(t, 0);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          ok = ok && wait_warp(&q_full[t], 0);
+          tc_fence_after();
+          if (ok && cnt_t[t] > 0) issue_qk(t, 0);
+        }
         tc_commit_if(lead, &k_empty[0]);
-        ok = wait_warp(&v_full[0], 0);
+        ok = ok && wait_warp(&v_full[0], 0);
       }
       for (int j = 0; j < cnt && ok; ++j) {
         const bool more = j + 1 < cnt;
@@ -421,28 +424,34 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax
     reg_inc<CONV ? 184 : 224>();
-    // first the queries: bf16 rows to fp16 tiles, 16 lanes a row, a warp the 32 rows it will work on
-#pragma unroll 1
-    for (int i0 = 0; i0 < 32; i0 += 16) {
+    // First the queries: bf16 rows to fp16 tiles, 16 lanes a row, a warp the 32 rows it will work on.  All loads
+    // first, and one division a lane (a load and two divisions a row in two rounds took 9600 cycles, an eighth of a
+    // block of a ragged prompt).
+    {
       const int ch = lane & 15;
-      uint4 w[8];
+      uint4 w[16];
+      const int rr0 = row_first + 32 * warp + (lane >> 4);
+      int tok = rr0 / a.group, gq = rr0 - tok * a.group;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 32 * warp + i0 + 2 * i + (lane >> 4);
+      for (int i = 0; i < 16; ++i) {
         w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < nrows) {
-          const int rr = row_first + r;
-          w[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(r0 + rr / a.group) * a.ldq +
-                                                      (int64_t)(head * a.group + rr % a.group) * kKv8Dim + 8 * ch));
+        if (32 * warp + 2 * i + (lane >> 4) < nrows)
+          w[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(r0 + tok) * a.ldq +
+                                                      (int64_t)(head * a.group + gq) * kKv8Dim + 8 * ch));
+        gq += 2;
+        while (gq >= a.group) {
+          gq -= a.group;
+          ++tok;
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 32 * warp + i0 + 2 * i + (lane >> 4);
+      for (int i = 0; i < 16; ++i) {
+        const int r = 32 * warp + 2 * i + (lane >> 4);
         const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
         uint32_t amax = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) amax = max(amax, max(ws[e] & 0x7FFFu, (ws[e] >> 16) & 0x7FFFu));
+        for (int e = 0; e < 4; ++e) amax = __vmaxu2(amax, ws[e] & 0x7FFF7FFFu);
+        amax = max(amax & 0xFFFFu, amax >> 16);
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
         float f, inv;
@@ -464,7 +473,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
     }
     fence_async_shared();
     __syncwarp();
-    if (lane == 0) mbar_arrive(q_full);
+    if (lane == 0) mbar_arrive(&q_full[warp >> 2]);
     const int t = warp >> 2;
     const int r = tid;                                          // row of the block
     const bool live = r < nrows;
@@ -580,7 +589,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
     ok = ok && (cnt == 0 || wait_warp(o_done, 0));
     tc_fence_after();
     if (ok) {
-      const int qh = head * a.group + rr % a.group;
+      const int gq = rr % a.group, qh = head * a.group + gq;
       const int64_t tok = r0 + rr / a.group;
       const int64_t fr = tok * a.q_heads + qh;
       const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
@@ -589,6 +598,9 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
         if (!whole) a.part_ml[fr * a.nsplit + split] = make_float2(m_run, l_run);
         else if (a.stats) a.stats[fr] = make_float2(m_run > -INFINITY ? m_run : 0.f, inv);
       }
+      // Whole rows go through the warp's 32 rows of its query tile's memory (read by the tensor core for the last time):
+      // written a row a thread, they leave two rows an instruction (straight to global memory they took 5200 cycles).
+      unsigned char* stage = smem + 32 * warp * 256;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t ov[32];
@@ -599,9 +611,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) ov[e] = 0u;
         }
-        if (!live) continue;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.o + tok * a.ldo + (int64_t)qh * kKv8Dim + 32 * q);
 #pragma unroll
           for (int e8 = 0; e8 < 4; ++e8) {
             uint32_t w[4];
@@ -611,12 +621,25 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
                                                               __uint_as_float(ov[8 * e8 + 2 * e2 + 1]) * inv);
               w[e2] = *reinterpret_cast<const uint32_t*>(&p2);
             }
-            dst[e8] = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * q + e8) ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else if (have) {
+        } else if (have && live) {
           uint4* dst = reinterpret_cast<uint4*>(a.part_o + (fr * a.nsplit + split) * kKv8Dim + 32 * q);
 #pragma unroll
           for (int e4 = 0; e4 < 8; ++e4) dst[e4] = make_uint4(ov[4 * e4], ov[4 * e4 + 1], ov[4 * e4 + 2], ov[4 * e4 + 3]);
+        }
+      }
+      if (whole) {
+        __syncwarp();
+        const int64_t at = tok * a.ldo + (int64_t)qh * kKv8Dim;      // of this lane's row
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int x = 2 * i + (lane >> 4), ch = lane & 15;
+          const int64_t to = __shfl_sync(0xffffffffu, at, x);
+          if (32 * warp + x < nrows)
+            *reinterpret_cast<uint4*>(a.o + to + 8 * ch) =
+                *reinterpret_cast<const uint4*>(stage + x * 256 + ((ch ^ (x & 7)) << 4));
         }
       }
     }
