@@ -965,7 +965,7 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({fill, steps / 8, 64}));
   p.image_steps = steps;
   const int64_t images = (int64_t)seqs * steps * heads;
-  p.prepare = p.nq == 0 && p.items >= kPrepareItems * (int64_t)busy && images * 2 * kTlTile <= kPrepareBytes;
+  p.prepare = p.nq == 0 && p.items >= kPrepareItems * (int64_t)busy && images <= kPrepareBytes / (2 * kTlTile);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;

@@ -199,10 +199,17 @@ class Int8KVCache:
         self._host[self.table.numel():] = torch.tensor([*before, *self._lens, *offsets], dtype=torch.int32)
         self._meta.copy_(self._host, non_blocking=True)
 
+    @staticmethod
+    def _not_captured() -> None:
+        """Bookkeeping is the host's: captured, a replay would repeat this step's."""
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("the cache's bookkeeping cannot be captured: prepare() before the capture and its replays")
+
     def prepare(self, counts: Sequence[int], append: bool = True) -> None:
         """Make counts[b] rows of every sequence b the subject of the next calls.  append=True: they join the
         cache (their pages are taken and the lengths grow now; append() must follow before attend()).
         append=False: nothing joins, they are the queries of the next attend()."""
+        self._not_captured()
         counts = [int(c) for c in counts]
         if len(counts) != self.sequences or any(c < 0 for c in counts):
             raise ValueError("counts must hold a number >= 0 for every sequence")
@@ -335,6 +342,7 @@ class Int8KVCache:
         accumulated weight (weights as attend() adds them up; cut to the kept tokens in place, zeros behind).  Needs
         free pages for the kept tokens; the old pages go back to the pool.  Returns int32 [sequences, heads, keep]:
         the positions kept, ascending, then -1.  Afterwards prepare() again."""
+        self._not_captured()
         if not 0 <= recent <= keep or keep <= 0:
             raise ValueError("0 <= recent <= keep and keep >= 1 are needed")
         if weights.device != self.codes.device:
@@ -367,6 +375,7 @@ class Int8KVCache:
 
     def release(self, sequence: int) -> None:
         """Empty a sequence; its pages go back to the pool.  Afterwards prepare() again."""
+        self._not_captured()
         if not 0 <= sequence < self.sequences:
             raise ValueError("no such sequence")
         self._free += reversed(self._pages[sequence])

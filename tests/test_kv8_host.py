@@ -208,6 +208,19 @@ def test_refused_calls_change_nothing(launches):
         R.Int8KVCache(1, 10, 1, pages=0, device="cpu")
 
 
+def test_bookkeeping_is_not_captured(launches, monkeypatch):
+    c = R.Int8KVCache(2, 200, 2, device="cpu")
+    c.prepare([3, 4])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    c.append(rows(7), rows(7))                           # launches alone
+    c.attend(rows(7), 2)
+    for f in (lambda: c.prepare([1, 1]), lambda: c.append(rows(7), rows(7), [3, 4]),
+              lambda: c.evict(torch.zeros(2, 2, 200), 2, 1), lambda: c.release(0)):
+        with pytest.raises(ValueError):
+            f()
+    assert c.lens == [3, 4]
+
+
 def test_binding_refuses_shapes_and_devices():
     codes, scales, table = torch.zeros(3, 2, 2, 64, 128, dtype=torch.uint8), torch.ones(3, 2, 2), torch.zeros(1, 3, dtype=torch.int32)
     for bad in (dict(codes=codes.int()), dict(codes=codes[:, :, :1]), dict(scales=scales[:2]), dict(scales=scales.double()),
