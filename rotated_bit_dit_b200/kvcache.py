@@ -245,15 +245,15 @@ class Int8KVCache:
     def append(self, k: torch.Tensor, v: torch.Tensor, counts: Optional[Sequence[int]] = None) -> None:
         """Quantise the prepared tokens' keys and values (bf16 [rows, >= heads*128], the sequences' rows one after
         another) into their pages; with counts, prepare(counts) first."""
-        # everything the call could be refused for, before the bookkeeping moves
-        for t in (k, v):
+        cur = self._current()
+        # with counts: everything the call could be refused for, before the bookkeeping moves
+        for t in (k, v) if counts is not None else ():
             if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] < self.heads * 128 or t.stride(1) != 1:
                 raise ValueError("k and v must be bf16 [rows, >= heads * 128], rows contiguous")
             if t.device != self._device:
                 raise ValueError(f"k or v is on {t.device}, the cache on {self._device}")
             if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
                 raise ValueError("rows of k and v must be 16-byte aligned")
-        cur = self._current()
         if counts is not None:
             if k.shape[0] != sum(int(c) for c in counts) or v.shape[0] != k.shape[0]:
                 raise ValueError("counts and rows differ")
