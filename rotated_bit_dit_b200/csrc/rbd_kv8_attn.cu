@@ -112,10 +112,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 //                      2 l + 8, 2 l + 9 of every 16: row g of product j is channel
 //                      16 g + 2 j, row g + 8 the next; P^T is the transposed scores'
 //                      fragment (one 8 x 8 transpose for 8 keys).
-// What bounds it is reading the cache once; close behind come the instructions that
-// convert codes (about 800 of a page's 1000 a warp), so what else a page needs (its
-// index, the logarithm and inverse of its scale) is worked out 32 pages at a time, one
-// a lane.
+// What bounds it is reading the cache once, and close behind a warp's own time for a
+// page (1260 instructions, 700 of them conversions, at three warps a scheduler), so
+// what else a page needs (its index, the logarithm and inverse of its scale) is
+// worked out 32 pages at a time, one a lane.  64 sequences of up to 8192 keys (292317
+// in all), 12 heads, 4 query heads each: 174 us, 5.2 TB/s; without the products 158
+// us, without the loads 139.
 constexpr uint32_t kStPage = 2 * kKv8Side;                           // 16 KB: a warp's two buffers
 constexpr int kStORow = kKv8Dim + 4;                                 // padded row of a warp's O in shared memory
 
