@@ -116,14 +116,18 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 // page (1260 instructions, 700 of them conversions, at three warps a scheduler), so
 // what else a page needs (its index, the logarithm and inverse of its scale) is
 // worked out 32 pages at a time, one a lane.  64 sequences of up to 8192 keys (292317
-// in all), 12 heads, 4 query heads each: 174 us, 5.2 TB/s; without the products 158
-// us, without the loads 139.
+// in all), 12 heads, 4 query heads each: 167 us, 5.4 TB/s (when it took 174: without
+// the products 158, without the loads 139).  24 sequences of up to 3000 keys, 8 heads, 1
+// to 6 tokens of 5 query heads each: 47 us, of which reading takes 14; a block there
+// has about four pages a warp, and the device less than two blocks an SM.
 constexpr uint32_t kStPage = 2 * kKv8Side;                           // 16 KB: a warp's two buffers
 constexpr int kStORow = kKv8Dim + 4;                                 // padded row of a warp's O in shared memory
 
 template <int NQ>
 struct StreamShape {
-  static constexpr int kWarps = NQ == 1 ? 12 : 8;                    // (of 8, registers for 16 rows: 12 spill, 54 us against 51)
+  // 16 rows want the registers of 8 warps: 12 spill (54 us against 51 for the 24 sequences above), and with the query
+  // fragments read from shared memory for every page instead gain nothing (51)
+  static constexpr int kWarps = NQ == 1 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NQ;
   static constexpr uint32_t kRing = kWarps * kStPage;
