@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kWgThreads, 2)
   for (int i = lane; i < b; i += 32) {
     int x0, xn;
     kv8_rows(a.cu, i, a.rows, x0, xn);
-    item0 += Kv8TileItems{a.group}(xn, 0);
+    item0 = min(a.items, item0 + Kv8TileItems{a.group}(xn, 0));
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) item0 += __shfl_xor_sync(0xffffffffu, item0, off);
@@ -751,7 +751,11 @@ __global__ void __launch_bounds__(kWgThreads, 2)
   const int nseen = max(0, (total + kTlRows - 1) / kTlRows - seen0);
   const int per = (nseen + parts - 1) / parts;
   const int tile0 = seen0 + part * per;
-  const int cnt = max(0, min(per, nseen - part * per));
+  // offsets that are not in order, so that sequences overlap, make more items than there are images
+  const int held = 2 * max(0, a.items - item0) - tile0;
+  const int mine = max(0, min(per, nseen - part * per));
+  const int cnt = max(0, min(mine, held));
+  if (cnt < mine && tid == 0) record_refusal();
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {

@@ -394,6 +394,23 @@ def test_device_side_metadata_is_refused_and_the_rest_is_right():
         assert torch.equal(cache.codes[mine], before[mine]) and torch.equal(cache.scales[mine], scales[mine])
 
 
+@pytest.mark.parametrize("rows,q_heads", [(300, 8), (40, 4), (3, 1)])
+def test_overlapping_offsets_are_refused(rows, q_heads):
+    """Offsets that go up and down give sequences that share rows, more of them than the launch is laid out for."""
+    rng = np.random.default_rng(29)
+    cache, plain = R.Int8KVCache(8, 512, 1), PlainCache(8, 1, 0)
+    fill(cache, plain, rng, [400] * 8)
+    cu = torch.tensor([0, rows] * 4 + [0], dtype=torch.int32, device="cuda")
+    q = dev(rand(rng, rows, q_heads))
+    o, w = torch.zeros_like(q), torch.zeros(8, 1, 512, device="cuda")
+    need = R.rbd_kv8_attn_workspace_bytes(8, 1, q_heads, rows, 512, True)
+    guard = torch.full((need + 4096,), 7, dtype=torch.uint8, device="cuda")
+    R.rbd_kv8_attn(q, cu, cache.device_lens, cache.table, cache.codes, cache.scales, o, q_heads, guard[:need], 512,
+                   weights_in=w, weights_out=w)
+    assert R.rbd_check() == 1 and R.rbd_check() == 0
+    assert bool((guard[need:] == 7).all())
+
+
 def test_rows_of_no_sequence_are_left_alone():
     rng = np.random.default_rng(13)
     cache, plain = R.Int8KVCache(2, 1024, 1), PlainCache(2, 1, 0)
