@@ -42,8 +42,10 @@ struct Kv8AttnArgs {
   const int32_t* lens;
   int rows, q_heads, group, causal, max_len, nsplit, items, seqs;
   float scale_log2;
-  float* part_o;       // [rows * q_heads][nsplit][128]: O of a split (null with one split)
-  float2* part_ml;     // [rows * q_heads][nsplit]: (m, L)
+  int whole;           // tile kernel: (head, item) pairs in front whose keys are not split
+  float* part_o;       // [slots][nsplit][128]: O of a split (null with one split); a slot is a (query token, head) in
+                       // the streaming kernel, a row of a split (head, item) in the tile kernel
+  float2* part_ml;     // [slots][nsplit]: (m, L)
   float2* stats;       // [rows * q_heads]: (m, 1 / L) of the whole row, or null
   float* logits;       // [rows * q_heads][logit_ld]: base-2 scores (stream kernel), or null
   int64_t logit_ld;
@@ -523,14 +525,11 @@ __global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kerne
   }
 }
 
-// Joins the splits of every (query token, head): a warp each, 4 channels a lane.
-__global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnArgs a) {
-  const int64_t fr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+// Joins the splits of query token `tok` and head `qh`, kept in `slot`: a warp, 4 channels a lane.
+__device__ __forceinline__ void kv8_join(const Kv8AttnArgs& a, int64_t slot, int64_t tok, int qh) {
   const int lane = threadIdx.x & 31;
-  if (fr >= (int64_t)a.rows * a.q_heads) return;
-  const int64_t tok = fr / a.q_heads;
-  if (tok < __ldg(a.cu) || tok >= __ldg(a.cu + a.seqs)) return;      // rows of no sequence stay as they are
-  const float2* ml = a.part_ml + fr * a.nsplit;          // at most 64 splits: two a lane
+  const int64_t fr = tok * a.q_heads + qh;
+  const float2* ml = a.part_ml + slot * a.nsplit;          // at most 64 splits: two a lane
   const float2 none = make_float2(-INFINITY, 0.f);
   const float2 x0 = lane < a.nsplit ? ml[lane] : none, x1 = lane + 32 < a.nsplit ? ml[lane + 32] : none;
   float m = fmaxf(x0.x, x1.x);
@@ -543,7 +542,7 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnArgs a) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* part = reinterpret_cast<const float4*>(a.part_o + fr * a.nsplit * kKv8Dim) + lane;
+  const float4* part = reinterpret_cast<const float4*>(a.part_o + slot * a.nsplit * kKv8Dim) + lane;
   for (int s0 = 0; s0 < a.nsplit; s0 += 4) {
     float4 u[4];
     float f[4];
@@ -565,9 +564,18 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnArgs a) {
   }
   const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;
   const __nv_bfloat162 p = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), q = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(a.o + tok * a.ldo + (fr - tok * a.q_heads) * kKv8Dim + 4 * lane) =
+  *reinterpret_cast<uint2*>(a.o + tok * a.ldo + (int64_t)qh * kKv8Dim + 4 * lane) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
   if (a.stats && lane == 0) a.stats[fr] = make_float2(m > -INFINITY ? m : 0.f, inv);
+}
+
+// Joins the splits of every (query token, head): a warp each.
+__global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnArgs a) {
+  const int64_t fr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (fr >= (int64_t)a.rows * a.q_heads) return;
+  const int64_t tok = fr / a.q_heads;
+  if (tok < __ldg(a.cu) || tok >= __ldg(a.cu + a.seqs)) return;      // rows of no sequence stay as they are
+  kv8_join(a, fr, tok, (int)(fr - tok * a.q_heads));
 }
 
 // weights_out = weights_in + sum of a key's weights over the queries and heads of

@@ -141,6 +141,21 @@ struct Kv8TileItems {
   }
 };
 
+// The (head, item) pair of a block, its split and the number of splits: first the blocks of whole pairs, then
+// those of the pairs behind them, whose keys are split.
+__device__ __forceinline__ int kv8_tile_place(const Kv8AttnArgs& a, int& head, int& split, int& nsplit) {
+  int at = blockIdx.x;
+  split = 0;
+  nsplit = 1;
+  if (at >= a.whole) {
+    nsplit = a.nsplit;
+    split = (at - a.whole) % nsplit;
+    at = a.whole + (at - a.whole) / nsplit;
+  }
+  head = at / a.items;
+  return at;
+}
+
 constexpr uint32_t kIdescBMn = 1u << 16;           // B is MN-major
 
 template <int N>
@@ -230,10 +245,11 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
   float* coef = reinterpret_cast<float*>(smem + kTlCoef);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int head = blockIdx.y, split = blockIdx.z;
+  int head, split, nsplit;
+  const int at = kv8_tile_place(a, head, split, nsplit);
   // items of a launch run from the last to the first: with a causal mask the later rows of a sequence see the
   // most keys, and long blocks had better start early
-  const int item = a.items - 1 - (int)blockIdx.x;
+  const int item = a.items - 1 - at % a.items;
   Kv8Item it;
   if (!kv8_find(a.cu, a.lens, c.seqs, a.rows, item, Kv8TileItems{a.group}, it)) return;
   const int b = it.b, tile = it.idx, r0 = it.r0, n = it.n;
@@ -249,7 +265,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
     steps[t] = (vis + kTlKeys - 1) / kTlKeys;
   }
   const int all = max(steps[0], steps[1]);
-  const int per = (all + a.nsplit - 1) / a.nsplit;
+  const int per = (all + nsplit - 1) / nsplit;
   const int j0 = split * per, j1 = min(all, j0 + per);
   const int cnt = max(0, j1 - j0);
   int cnt_t[2];
@@ -599,9 +615,10 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
       const int64_t tok = r0 + rr / a.group;
       const int64_t fr = tok * a.q_heads + qh;
       const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
-      const bool whole = a.nsplit == 1;
+      const bool whole = nsplit == 1;
+      const int64_t slot = ((int64_t)(at - a.whole) * 2 * kTlRows + r) * nsplit + split;
       if (live) {
-        if (!whole) a.part_ml[fr * a.nsplit + split] = make_float2(m_run, l_run);
+        if (!whole) a.part_ml[slot] = make_float2(m_run, l_run);
         else if (a.stats) a.stats[fr] = make_float2(m_run > -INFINITY ? m_run : 0.f, inv);
       }
       // Whole rows go through the warp's 32 rows of its query tile's memory (read by the tensor core for the last time):
@@ -631,7 +648,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (have && live) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + (fr * a.nsplit + split) * kKv8Dim + 32 * q);
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + slot * kKv8Dim + 32 * q);
 #pragma unroll
           for (int e4 = 0; e4 < 8; ++e4) dst[e4] = make_uint4(ov[4 * e4], ov[4 * e4 + 1], ov[4 * e4 + 2], ov[4 * e4 + 3]);
         }
@@ -656,6 +673,16 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the splits of the pairs that have them: a warp a row.
+__global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const Kv8AttnArgs a) {
+  const int at = a.whole + (int)blockIdx.x, r = (int)(blockIdx.y * 8 + (threadIdx.x >> 5));
+  Kv8Item it;
+  if (!kv8_find(a.cu, a.lens, a.seqs, a.rows, a.items - 1 - at % a.items, Kv8TileItems{a.group}, it)) return;
+  const int rr = it.idx * 2 * kTlRows + r;
+  if (rr >= it.n * a.group) return;
+  kv8_join(a, (int64_t)blockIdx.x * 2 * kTlRows + r, it.r0 + rr / a.group, at / a.items * a.group + rr % a.group);
 }
 
 // ---------------------------------------------------------------------------
@@ -944,6 +971,7 @@ __global__ void __launch_bounds__(256)
 struct Kv8Plan {
   int nq;              // streaming kernel with 8 nq rows a block; 0: the tile kernel
   int items, nsplit;
+  int whole;           // tile kernel: (head, item) pairs whose keys are not split
   bool prepare;        // operand images
   int image_steps;     // 128-key steps of a sequence in them
   int parts;           // parts of a key block's query tiles
@@ -965,7 +993,8 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   p.nq = packed <= 8 * (int64_t)seqs ? 1 : packed <= (int64_t)kStreamRows * seqs ? 2 : 0;
   const int unit = p.nq ? 8 * p.nq : 2 * kTlRows;
   const int busy = std::min(seqs, rows);             // sequences that can have queries
-  p.items = (int)std::min<int64_t>(packed, packed / unit + busy);
+  // the most that sequences of at least one row each can have
+  p.items = (int)std::min<int64_t>(packed, std::max<int64_t>(packed - busy, 0) / unit + busy);
   const int64_t blocks = (int64_t)p.items * heads;
   const int steps = std::max(1, (max_len + kTlKeys - 1) / kTlKeys);
   // A split costs its partial result and, with tiles, another setup of the block: the streaming kernel splits into
@@ -975,6 +1004,22 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   const int64_t fill = p.nq ? (blocks < 148 * 2 ? (148 * 4 + blocks - 1) / std::max<int64_t>(blocks, 1) : 1)
                             : 148 / std::max<int64_t>(blocks, 1);
   p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({fill, steps / 8, 64}));
+  p.whole = p.nsplit > 1 ? 0 : (int)blocks;
+  // Blocks of a tile kernel that last alike run in waves, and the last wave may be nearly empty.  Its blocks are split
+  // when that is shorter by an estimate in steps: a block's setup counts as four, the join as two and 1/32 for every
+  // split.  Blocks last alike where a sequence's queries are few beside its keys.
+  const int tail = (int)(blocks % 148);
+  if (p.nq == 0 && blocks > 148 && tail > 0 && 2 * (int64_t)rows <= (int64_t)max_len * busy) {
+    int64_t best = 32 * (int64_t)(steps + 4);
+    for (int k = 2; k <= std::min(8, steps / 8); ++k) {
+      const int64_t cost = 32 * (int64_t)((tail * k + 147) / 148 * ((steps + k - 1) / k + 4) + 2) + tail * k;
+      if (cost < best) {
+        best = cost;
+        p.nsplit = k;
+        p.whole = (int)blocks - tail;
+      }
+    }
+  }
   p.image_steps = steps;
   const int64_t images = (int64_t)seqs * steps * heads;
   p.prepare = p.nq == 0 && p.items >= kPrepareItems * (int64_t)busy && images <= kPrepareBytes / (2 * kTlTile);
@@ -985,8 +1030,9 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
     return o;
   };
   const int64_t fr = (int64_t)rows * q_heads;
-  p.part_o = p.nsplit > 1 ? take(fr * p.nsplit * kKv8Dim * 4) : -1;
-  p.part_ml = p.nsplit > 1 ? take(fr * p.nsplit * 8) : -1;
+  const int64_t slots = p.nq ? fr : (blocks - p.whole) * 2 * kTlRows;
+  p.part_o = p.nsplit > 1 ? take(slots * p.nsplit * kKv8Dim * 4) : -1;
+  p.part_ml = p.nsplit > 1 ? take(slots * p.nsplit * 8) : -1;
   p.stats = weigh ? take(fr * 8) : -1;
   p.logit_ld = (max_len + kKv8Page - 1) / kKv8Page * (int64_t)kKv8Page;
   p.logits = weigh && p.nq ? take(fr * p.logit_ld * 4) : -1;
@@ -1022,7 +1068,8 @@ cudaError_t launch_kv8_attn_fmt(const Kv8View& c, const Kv8AttnArgs& a, const Kv
                                 float* w_out, int64_t w_seq, int64_t w_head, void* work, cudaStream_t st) {
   cudaError_t e;
   if (a.rows > 0) {
-    const dim3 grid(p.items, c.heads, p.nsplit);
+    const int split_pairs = p.items * c.heads - p.whole;
+    const dim3 grid = p.nq ? dim3(p.items, c.heads, p.nsplit) : dim3(p.whole + split_pairs * p.nsplit);
     if (p.nq) {
       e = p.nq == 1 ? launch_stream<FMT, 1>(grid, c, a, st) : launch_stream<FMT, 2>(grid, c, a, st);
       if (e != cudaSuccess) return e;
@@ -1040,7 +1087,9 @@ cudaError_t launch_kv8_attn_fmt(const Kv8View& c, const Kv8AttnArgs& a, const Kv
         kv8_tile_kernel<FMT, true><<<grid, kTlConvThreads, kTlSmem, st>>>(c, a);
       }
     }
-    if (p.nsplit > 1) {
+    if (p.nsplit > 1 && p.nq == 0) {
+      kv8_tile_combine_kernel<<<dim3(split_pairs, 2 * kTlRows / 8), 256, 0, st>>>(a);
+    } else if (p.nsplit > 1) {
       const int64_t fr = (int64_t)a.rows * a.q_heads;
       kv8_combine_kernel<<<(unsigned)((fr + 7) / 8), 256, 0, st>>>(a);
     }
@@ -1087,6 +1136,7 @@ cudaError_t launch_kv8_attn(const Kv8View& c, bool e4m3, const int32_t* lens, co
   a.seqs = c.seqs;
   a.max_len = max_len;
   a.nsplit = p.nsplit;
+  a.whole = p.whole;
   a.items = p.items;
   a.scale_log2 = scale_log2;
   a.part_o = reinterpret_cast<float*>(at(p.part_o));

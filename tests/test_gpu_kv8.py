@@ -192,6 +192,41 @@ def test_attend_keys_shared_by_many_blocks(fmt, causal, held, new, heads, group)
     check_attend(cache, plain, rng, new, heads * group, causal, q_gain=1.5, weights=w)
 
 
+@pytest.mark.parametrize("fmt,causal", [(0, True), (1, False)])
+@pytest.mark.parametrize("heads,group,held,new", [
+    (1, 64, [2100, 600, 2, 0, 900], [620, 30, 3, 2, 0]),                       # 169 blocks, operand images
+    (2, 32, [2100] + [70, 130, 300] * 13, [12] * 40),                          # 198 blocks that convert for themselves
+])
+def test_blocks_of_a_last_wave_share_their_keys(fmt, causal, heads, group, held, new):
+    """More blocks than processors: the blocks behind the last full wave have their keys split."""
+    rng = np.random.default_rng(31)
+    cache, plain = R.Int8KVCache(len(held), 2112, heads, code_format=fmt), PlainCache(len(held), heads, fmt)
+    fill(cache, plain, rng, held)
+    rows, q_heads = sum(new), heads * group
+    assert R.rbd_kv8_attn_workspace_bytes(len(held), heads, q_heads, rows, 2100) > 0
+    q = rand(rng, rows, q_heads)
+    cache.prepare(new, append=False)
+    w = torch.zeros((len(held), heads, 2112), device="cuda")
+    got = cache.attend(dev(q), q_heads, causal=causal, weights=w)
+    again = cache.attend(dev(q), q_heads, causal=causal)
+    assert R.rbd_check() == 0 and torch.equal(got, again)
+    got = got.float().cpu().numpy().reshape(rows, q_heads, 128)
+    picks = [[(17 * i + 5 * j) % group for j in range(3)] for i in range(heads)]       # of every cache head's queries
+    at = 0
+    for b, n in enumerate(new):
+        some = q[at:at + n].reshape(n, heads, group, 128)
+        part = np.stack([some[:, i, picks[i]] for i in range(heads)], 1).reshape(n, 3 * heads, 128)
+        o, _, eo, _ = plain.attend(b, part.astype(np.float64), 3 * heads, causal)
+        mine = got[at:at + n].reshape(n, heads, group, 128)
+        mine = np.stack([mine[:, i, picks[i]] for i in range(heads)], 1).reshape(n, 3 * heads, 128)
+        assert (np.abs(mine - o) <= eo + 1e-30).all(), b
+        at += n
+        # a row that sees a key adds one to the sum of its weights: a float32 sum of `held` terms each way
+        sums = w[b].double().sum(1).cpu().numpy()
+        live = min(n, held[b]) if causal else (n if held[b] else 0)
+        assert (np.abs(sums - live * group) <= live * group * ((held[b] + n * group) * 2.0 ** -23 + 2.0 ** -20) + 1e-30).all(), b
+
+
 def evict_case(rng, fmt, lens, heads, keep, recent, weights, in_place=False):
     """Entry-level eviction of a filled cache against the plain one; returns nothing, asserts everything."""
     n, width = len(lens), weights.shape[2]
