@@ -997,21 +997,22 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   p.items = (int)std::min<int64_t>(packed, std::max<int64_t>(packed - busy, 0) / unit + busy);
   const int64_t blocks = (int64_t)p.items * heads;
   const int steps = std::max(1, (max_len + kTlKeys - 1) / kTlKeys);
-  // A split costs its partial result and, with tiles, another setup of the block: the streaming kernel splits into
-  // four blocks an SM where there are fewer than two (3 sequences of up to 120001 keys: 104 us, 115 with two a
-  // SM; 24 sequences x 8 heads x 2 blocks: 55 us unsplit, 67 split in two), the tile kernel only to fill the device
-  // once.  At least eight 128-key steps each.
-  const int64_t fill = p.nq ? (blocks < 148 * 2 ? (148 * 4 + blocks - 1) / std::max<int64_t>(blocks, 1) : 1)
-                            : 148 / std::max<int64_t>(blocks, 1);
-  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({fill, steps / 8, 64}));
-  p.whole = p.nsplit > 1 ? 0 : (int)blocks;
-  // Blocks of a tile kernel that last alike run in waves, and the last wave may be nearly empty.  Its blocks are split
-  // when that is shorter by an estimate in steps: a block's setup counts as four, the join as two and 1/32 for every
-  // split.  Blocks last alike where a sequence's queries are few beside its keys.
-  const int tail = (int)(blocks % 148);
-  if (p.nq == 0 && blocks > 148 && tail > 0 && 2 * (int64_t)rows <= (int64_t)max_len * busy) {
+  p.nsplit = 1;
+  p.whole = (int)blocks;
+  if (p.nq) {
+    // A split costs its partial result: the streaming kernel splits into four blocks an SM where there are fewer than
+    // two, at least eight 128-key steps each (3 sequences of up to 120001 keys: 104 us, 115 with two a SM; 24
+    // sequences x 8 heads x 2 blocks: 55 us unsplit, 67 split in two).
+    if (blocks > 0 && blocks < 148 * 2)
+      p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({(148 * 4 + blocks - 1) / blocks, steps / 8, 64}));
+  } else if (blocks <= 148 || 2 * (int64_t)rows <= (int64_t)max_len * busy) {
+    // Blocks of the tile kernel that last alike (where a sequence's queries are few beside its keys) run in waves.
+    // Those of a last, partly filled wave are split when that is shorter by an estimate in steps: a block's setup
+    // counts as four, the join as two and 1/32 for every split (4096 queries over 16384 keys x 24 heads, 384 blocks:
+    // 756 us whole, 711 with the last 88 split in three; 1024 queries, 96 blocks: 294 us whole, 261 split in three).
+    const int tail = (int)(blocks % 148);
     int64_t best = 32 * (int64_t)(steps + 4);
-    for (int k = 2; k <= std::min(8, steps / 8); ++k) {
+    for (int k = 2; tail > 0 && k <= std::min(64, steps / 8); ++k) {
       const int64_t cost = 32 * (int64_t)((tail * k + 147) / 148 * ((steps + k - 1) / k + 4) + 2) + tail * k;
       if (cost < best) {
         best = cost;
