@@ -25,7 +25,7 @@
 //                      the cache once.  Warps stream pages from memory.
 //   kv8_tile_kernel    more: bound by the tensor cores (tcgen05).
 // Both split the keys over several blocks when there are few items and write
-// float32 partial results, which kv8_combine_kernel joins.
+// float32 partial results, which kv8_combine_kernel and kv8_tile_combine_kernel join.
 #include <algorithm>
 
 #include "rbd_kv8.cuh"

@@ -20,8 +20,8 @@
 // pipe (4096 queries over 16384 keys x 24 heads: 2157 us against 748 without softmax
 // and converters).  Where it is used once, the images' traffic (5 bytes a value
 // against 1) would dominate, and the block converts for itself.
-// Measured: 4096 queries over 16384 keys x 24 heads in 753 us with the images (47 of
-// it), 1.10 PFLOP/s, the tensor pipe 63% busy.  What bounds it is the chain of a query
+// Measured: 4096 queries over 16384 keys x 24 heads in 711 us with the images (47 of
+// it) and the join of what is split (15), 1.16 PFLOP/s, the tensor pipe 63% busy.  What bounds it is the chain of a query
 // tile: a softmax step (128 scores a thread, about 2000 cycles, 1275 of them
 // exponentials) and then its P.V and Q.K^T (1024), of which the other tile hides the
 // latter; of a ragged causal prompt (21186 tokens x 48 heads: 971 us, 0.88 PFLOP/s)
