@@ -992,7 +992,8 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
   const int64_t packed = (int64_t)rows * group;
   p.nq = packed <= 8 * (int64_t)seqs ? 1 : packed <= (int64_t)kStreamRows * seqs ? 2 : 0;
   const int unit = p.nq ? 8 * p.nq : 2 * kTlRows;
-  const int busy = std::min(seqs, rows);             // sequences that can have queries
+  // sequences that can have queries (one where there is no row at all: it divides below)
+  const int busy = std::max(1, std::min(seqs, rows));
   // the most that sequences of at least one row each can have
   p.items = (int)std::min<int64_t>(packed, std::max<int64_t>(packed - busy, 0) / unit + busy);
   const int64_t blocks = (int64_t)p.items * heads;

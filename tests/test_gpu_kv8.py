@@ -549,3 +549,20 @@ def test_two_streams_at_once():
         assert R.rbd_check() == 0
         for (_, y), x in zip(got, [want[0], want[2], want[1], want[3]]):
             assert torch.equal(y, x)
+
+
+def test_a_step_without_rows():
+    """No sequence has a row: nothing is attended to, and weights_out becomes weights_in over the tokens held."""
+    rng = np.random.default_rng(30)
+    cache, plain = R.Int8KVCache(3, 512, 2), PlainCache(3, 2, 0)
+    fill(cache, plain, rng, [300, 0, 70])
+    none = torch.empty((0, 4 * 128), dtype=torch.bfloat16, device="cuda")
+    cache.append(none[:, :256], none[:, :256], [0, 0, 0])
+    check_codes(cache, plain)
+    w = torch.rand((3, 2, 512), device="cuda")
+    out = torch.full_like(w, -3.0)
+    assert cache.attend(none, 4).shape == (0, 512)
+    assert cache.attend(none, 4, weights=w, weights_out=out).shape == (0, 512)
+    assert R.rbd_check() == 0
+    for b, n in enumerate([300, 0, 70]):
+        assert torch.equal(out[b, :, :n], w[b, :, :n]) and bool((out[b, :, n:] == -3).all())

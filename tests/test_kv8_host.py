@@ -239,3 +239,20 @@ def test_binding_refuses_shapes_and_devices():
     for bad in (w.double(), w[0], w[:, :2], w.transpose(1, 2)):
         with pytest.raises(ValueError):
             B._weights(bad, 2, 3, "w")
+
+
+@pytest.mark.parametrize("weigh", [False, True])
+@pytest.mark.parametrize("length", [0, 1, 512, 1 << 20])
+@pytest.mark.parametrize("seqs,heads,q_heads", [(1, 1, 1), (2, 4, 8), (65535, 1024, 65536)])
+def test_workspace_of_no_rows(seqs, heads, q_heads, length, weigh):
+    """A step in which no sequence has a row: nothing is split, scored or imaged."""
+    assert R.rbd_kv8_attn_workspace_bytes(seqs, heads, q_heads, 0, length, weigh) == 0
+
+
+def test_a_step_without_rows(launches):
+    c = R.Int8KVCache(3, 300, 2, device="cpu")
+    c.append(rows(70), rows(70), [64, 0, 6])
+    c.append(rows(0), rows(0), [0, 0, 0])
+    assert c.attend(rows(0, 4), 4).shape == (0, 512)
+    assert c.attend(rows(0, 4), 4, weights=torch.zeros(3, 2, 300)).shape == (0, 512)
+    assert c.lens == [64, 0, 6] and launches == ["append", "append", "attn", "attn"]
