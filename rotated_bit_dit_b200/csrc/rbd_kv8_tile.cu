@@ -608,7 +608,9 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
     }
     // output: O / L, or the split's O, m and L
     const bool have = mine > 0;
-    ok = ok && (cnt == 0 || wait_warp(o_done, 0));
+    // A block whose rows see no key has no products to wait for, but the rows below are staged over queries that the
+    // tile's other warps may still be writing.
+    ok = ok && wait_warp(&q_full[t], 0) && (cnt == 0 || wait_warp(o_done, 0));
     tc_fence_after();
     if (ok) {
       const int gq = rr % a.group, qh = head * a.group + gq;
@@ -621,7 +623,8 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
         if (!whole) a.part_ml[slot] = make_float2(m_run, l_run);
         else if (a.stats) a.stats[fr] = make_float2(m_run > -INFINITY ? m_run : 0.f, inv);
       }
-      // Whole rows go through the warp's 32 rows of its query tile's memory (read by the tensor core for the last time):
+      // Whole rows go through 8 KB of the query tile's memory, which holds rows of other warps of the tile (all written
+      // by now, and read by the tensor core for the last time):
       // written a row a thread, they leave two rows an instruction (straight to global memory they took 5200 cycles).
       unsigned char* stage = smem + 32 * warp * 256;
 #pragma unroll

@@ -566,3 +566,25 @@ def test_a_step_without_rows():
     assert R.rbd_check() == 0
     for b, n in enumerate([300, 0, 70]):
         assert torch.equal(out[b, :, :n], w[b, :, :n]) and bool((out[b, :, n:] == -3).all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("held", [0, 40])
+def test_rows_that_see_no_key_are_zeros_every_time(fmt, held):
+    """Blocks of 256 rows that see no key (an empty sequence, or the queries in front of a short one's first token):
+    zeros, whichever of a block's warps fetches its queries last."""
+    rng = np.random.default_rng(32)
+    heads, group, n = 2, 3, 5000
+    cache, plain = R.Int8KVCache(2, 1024, heads, code_format=fmt), PlainCache(2, heads, fmt)
+    fill(cache, plain, rng, [held, 900])
+    q = dev(rand(rng, n + 600, heads * group))
+    cache.prepare([n, 600], append=False)
+    first = None
+    for _ in range(20):
+        out = torch.full((n + 600, heads * group * 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        cache.attend(q, heads * group, out=out)
+        assert not out[:n - held].any()
+        assert bool(out[n - held:].any(dim=1).all())
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    assert R.rbd_check() == 0
