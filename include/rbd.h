@@ -493,7 +493,8 @@ int64_t rbd_kv8_attn_workspace_bytes(int64_t seqs, int64_t heads, int64_t q_head
  *           reads cache head j / (q_heads / heads); ld % 8 == 0, 16-byte aligned.
  *   causal  nonzero: the n queries of a sequence are its last n tokens, query i
  *           sees tokens 0 .. lens[b] - n + i; zero: every query sees all tokens.
- *           A query that sees no token gets zeros.
+ *           A query that sees no token gets zeros, one with an infinite or NaN element
+ *           that sees any NaN (and so do the weights of the keys it sees).
  *   max_len at least every lens[b] (a longer one is refused on the device); the
  *           launch is laid out for it, so that a captured call stays right for
  *           any lengths up to it.

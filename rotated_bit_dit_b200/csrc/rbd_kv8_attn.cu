@@ -64,12 +64,14 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// The power of two that brings a row whose largest |bf16| has bits `amax` to [2^14, 2^15), and its inverse.
+// The power of two that brings a row whose largest |bf16| has bits `amax` to [2^14, 2^15), and its inverse.  A row
+// with an infinite or NaN element has scores that are infinite or NaN, and by the definition a softmax of NaN: a NaN
+// inverse, a factor of every score, says so (infinite scores by themselves vanish against an infinite maximum).
 __device__ __forceinline__ void kv8_row_scale(uint32_t amax, float& f, float& inv) {
   const int e = (int)(amax >> 7);
   const int field = min(268 - e, 253);
   f = __uint_as_float((uint32_t)field << 23);
-  inv = __uint_as_float((uint32_t)(254 - field) << 23);
+  inv = __uint_as_float(e == 255 ? 0x7FFFFFFFu : (uint32_t)(254 - field) << 23);
 }
 
 // A sequence's length, or 0 (recorded) when it exceeds what the call declared.

@@ -588,3 +588,38 @@ def test_rows_that_see_no_key_are_zeros_every_time(fmt, held):
         first = out if first is None else first
         assert torch.equal(out, first)
     assert R.rbd_check() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,held", [(1, 300), (12, 300), (200, 300), (200, 2), (1, 5000), (300, 5000)])
+def test_an_infinite_query_gives_nan_in_its_row(fmt, causal, n, held):
+    """Its scores are infinite (or NaN, against a zero): the softmax over them is NaN, wherever the infinities stand,
+    and so are the weights of the keys the row sees; other rows and the keys it does not see are left alone."""
+    rng = np.random.default_rng(33)
+    cache, plain = R.Int8KVCache(1, 5120, 1, code_format=fmt), PlainCache(1, 1, fmt)
+    for lucky in (np.arange(held) % 8 == 6, np.arange(held) % 8 == 7, np.arange(held) == 6, np.zeros(held, bool),
+                  np.ones(held, bool)):
+        if cache.lens[0]:
+            cache.release(0)
+            plain = PlainCache(1, 1, fmt)
+        k, v = rand(rng, held, 1), rand(rng, held, 1)
+        k[:, 0, 3] = np.where(lucky, 4.0, -4.0)          # the sign of the score against +inf in channel 3
+        cache.append(dev(k), dev(v), [held])
+        plain.append(0, k, v)
+        q = rand(rng, n, 2)
+        clean = check_attend(cache, plain, rng, [n], 2, causal, q=q)
+        row = n // 2
+        q[row, 1, 3] = np.inf
+        w = torch.zeros((1, 1, 5120), device="cuda")
+        got = cache.attend(dev(q), 2, causal=causal).float().cpu().numpy().reshape(n, 2, 128)
+        also = cache.attend(dev(q), 2, causal=causal, weights=w).float().cpu().numpy().reshape(n, 2, 128)
+        assert R.rbd_check() == 0
+        sees = max(0, held - n + row + 1) if causal else held
+        keep = np.ones((n, 2), bool)
+        keep[row, 1] = False
+        for y in (got, also):
+            assert np.isnan(y[row, 1]).all() if sees else not y[row, 1].any()
+            assert np.array_equal(y[keep], clean[keep])
+        w = w[0, 0].cpu().numpy()
+        assert np.isnan(w[:sees]).all() and np.isfinite(w[sees:]).all()
