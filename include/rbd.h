@@ -501,7 +501,9 @@ int64_t rbd_kv8_attn_workspace_bytes(int64_t seqs, int64_t heads, int64_t q_head
  *   weights_in, weights_out  both NULL, or float32 with element (b, h, t) at
  *           b * w_seq + h * w_head + t, w_head >= max_len: weights_out = weights_in +
  *           the sum, over the queries of sequence b and the query heads of cache
- *           head h, of the weight key t got; t < lens[b] only.  They may be the same.
+ *           head h, of the weight key t got; t < lens[b] only.  They are the same, or have
+ *           no element in common; no two (b, h) share one, so one of the strides spans
+ *           all rows of the other.
  *   work    rbd_kv8_attn_workspace_bytes(...) bytes, 256-byte aligned (NULL if 0):
  *           float32 partial results where keys are split; with weights and few rows
  *           a sequence 4 bytes per (row, query head, key up to max_len); with many
@@ -523,8 +525,9 @@ rbd_status rbd_kv8_attn(const rbd_kv8* cache, const int32_t* lens, const int32_t
  *               kept tokens (quantised as by append from code * scale).  None may be
  *               a page the sequences hold.
  *   kept        int32 [seqs, heads, keep]: positions kept, ascending, then -1.
- *   weights_out float32 (strides o_seq, o_head; width_out >= keep columns): the kept
- *               tokens' weights, then zeros; may be `weights`.
+ *   weights_out float32 (strides o_seq, o_head; width_out >= keep columns, no two (b, h)
+ *               sharing one): the kept tokens' weights, then zeros; `weights` itself
+ *               (of the same strides), or apart from it.
  *   lens_out    int32 [seqs]: min(lens, keep); not `lens` itself.
  * 0 <= recent <= keep, keep >= 1.                                             */
 rbd_status rbd_kv8_evict(const rbd_kv8* cache, const int32_t* lens, const float* weights, int64_t w_seq,

@@ -4,6 +4,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include <cudaTypedefs.h>
 
@@ -631,6 +632,39 @@ rbd_status kv8_view(const rbd_kv8* c, rbd::Kv8View* out, bool* e4m3) {
   return RBD_OK;
 }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Key weights are rows (b, h) of floats at b * seq + h * head.  True when no two rows of `cols` floats share an
+// element: one of the strides spans all rows of the other.
+bool rows_apart(int64_t seqs, int64_t heads, int64_t seq, int64_t head, int64_t cols) {
+  if (cols == 0) return true;
+  if ((seqs > 1 && seq < cols) || (heads > 1 && head < cols)) return false;
+  return seqs == 1 || heads == 1 || (seq - cols) / (heads - 1) >= head || (head - cols) / (seqs - 1) >= seq;
+}
+
+// True when rows of `in_cols` floats at `in` and of `out_cols` at `out`, of the same strides and apart among
+// themselves, share an element.
+bool rows_meet(int64_t seqs, int64_t heads, int64_t seq, int64_t head, const float* in, int64_t in_cols,
+               const float* out, int64_t out_cols) {
+  int64_t n[2] = {seqs, heads}, step[2] = {seq, head};        // the stride that spans the other's rows first
+  if (n[0] == 1 || (n[1] > 1 && step[0] < step[1])) {
+    std::swap(n[0], n[1]);
+    std::swap(step[0], step[1]);
+  }
+  const int64_t shift = (reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(in)) / 4;
+  auto near = [](int64_t d, int64_t s) { return d / s - (d % s < 0); };     // row difference just below d
+  const int64_t i0 = n[0] > 1 ? near(shift, step[0]) : 0;
+  for (int64_t i = i0; i <= i0 + (n[0] > 1); ++i) {
+    if (i <= -n[0] || i >= n[0]) continue;
+    const int64_t rest = shift - i * step[0];
+    const int64_t j0 = n[1] > 1 ? near(rest, step[1]) : 0;
+    for (int64_t j = j0; j <= j0 + (n[1] > 1); ++j) {
+      if (j <= -n[1] || j >= n[1]) continue;
+      const int64_t d = rest - j * step[1];
+      if (d < in_cols && d > -out_cols) return true;
+    }
+  }
+  return false;
+}
 }  // namespace
 
 rbd_status rbd_kv8_append(const rbd_kv8* cache, const int32_t* lens, const int32_t* cu, const void* k, int64_t ldk,
@@ -700,6 +734,12 @@ rbd_status rbd_kv8_attn(const rbd_kv8* cache, const int32_t* lens, const int32_t
     return RBD_ERR_INVALID_ARG;
   const bool weigh = weights_out != nullptr;
   if (weigh && (w_head < max_len || w_seq < 0)) return RBD_ERR_INVALID_ARG;
+  // keys' weights are written by many blocks at once: every one in a place of its own
+  if (weigh && c.seqs > 0 &&
+      (!rows_apart(c.seqs, c.heads, w_seq, w_head, max_len) ||
+       (weights_in != weights_out && max_len > 0 &&
+        rows_meet(c.seqs, c.heads, w_seq, w_head, weights_in, max_len, weights_out, max_len))))
+    return RBD_ERR_INVALID_ARG;
   if (c.seqs == 0 || (rows == 0 && !weigh)) return RBD_OK;
   if (!lens || !cu || (rows > 0 && (!q || !o || ldq < q_heads * 128 || ldo < q_heads * 128))) return RBD_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || (ldq % 8) || (ldo % 8) || !aligned4(lens) || !aligned4(cu) ||
@@ -729,9 +769,20 @@ rbd_status rbd_kv8_evict(const rbd_kv8* cache, const int32_t* lens, const float*
   if (c.seqs == 0) return RBD_OK;
   if (!lens || !weights || !dst_table || !kept || !weights_out || !lens_out) return RBD_ERR_INVALID_ARG;
   if (lens_out == lens) return RBD_ERR_INVALID_ARG;     // read by blocks that may run after it is written
+  // the kept tokens' weights are written by many blocks at once, each over its own row of `weights` at most
+  if (!rows_apart(c.seqs, c.heads, o_seq, o_head, width_out)) return RBD_ERR_INVALID_ARG;
   if (!aligned4(lens) || !aligned4(weights) || !aligned4(dst_table) || !aligned4(kept) || !aligned4(weights_out) ||
       !aligned4(lens_out))
     return RBD_ERR_ALIGNMENT;
+  const bool alike = (c.seqs == 1 || w_seq == o_seq) && (c.heads == 1 || w_head == o_head) &&
+                     rows_apart(c.seqs, c.heads, w_seq, w_head, width);
+  if (alike && weights != weights_out) {
+    if (rows_meet(c.seqs, c.heads, o_seq, o_head, weights, width, weights_out, width_out)) return RBD_ERR_INVALID_ARG;
+  } else if (!alike) {
+    const float* w_end = weights + (c.seqs - 1) * w_seq + (c.heads - 1) * w_head + width;
+    const float* o_end = weights_out + (c.seqs - 1) * o_seq + (c.heads - 1) * o_head + width_out;
+    if (weights < o_end && weights_out < w_end) return RBD_ERR_INVALID_ARG;
+  }
   return cuda_status(rbd::launch_kv8_evict(c, e4m3, weights, w_seq, w_head, static_cast<int>(width), weights_out,
                                            o_seq, o_head, static_cast<int>(width_out), lens, lens_out, kept,
                                            static_cast<int>(keep), static_cast<int>(recent), dst_table, ld_dst,

@@ -623,3 +623,43 @@ def test_an_infinite_query_gives_nan_in_its_row(fmt, causal, n, held):
             assert np.array_equal(y[keep], clean[keep])
         w = w[0, 0].cpu().numpy()
         assert np.isnan(w[:sees]).all() and np.isfinite(w[sees:]).all()
+
+
+def test_weights_in_any_layout_and_none_that_overlap():
+    """Weights whose heads lie outside the sequences, and in and out interleaved in one buffer: as in a layout of
+    their own.  Expanded ones are refused, and an eviction refused for them moves no pages."""
+    rng = np.random.default_rng(34)
+    seqs, heads, width = 3, 2, 512
+    cache, plain = R.Int8KVCache(seqs, width, heads, pages=40), PlainCache(seqs, heads, 0)
+    fill(cache, plain, rng, [300, 70, 500])
+    cache.prepare([2, 1, 40], append=False)
+    q = dev(rand(rng, 43, heads))
+    w = torch.rand((seqs, heads, width), device="cuda")
+    want = torch.zeros_like(w)
+    o = cache.attend(q, heads, weights=w, weights_out=want)
+    turned = torch.zeros((heads, seqs, width), device="cuda").transpose(0, 1)
+    turned.copy_(w)
+    cache.attend(q, heads, weights=turned)
+    both = torch.zeros((seqs, 2, heads, width), device="cuda")
+    both[:, 0] = w
+    assert torch.equal(cache.attend(q, heads, weights=both[:, 0], weights_out=both[:, 1]), o)
+    for b, n in enumerate([300, 70, 500]):
+        assert torch.equal(turned[b, :, :n], want[b, :, :n]) and torch.equal(both[b, 1, :, :n], want[b, :, :n])
+    assert torch.equal(both[:, 0], w)
+    for bad in (w[:1].expand(seqs, heads, width), w[:, :1].expand(seqs, heads, width)):
+        with pytest.raises(R.RbdError):
+            cache.attend(q, heads, weights=bad)
+        with pytest.raises(R.RbdError):
+            cache.evict(bad, 100, 10)
+    flat = torch.zeros(seqs * heads * width + 1, device="cuda")
+    with pytest.raises(R.RbdError):
+        cache.attend(q, heads, weights=flat[:-1].view(seqs, heads, width), weights_out=flat[1:].view(seqs, heads, width))
+    assert cache.lens == [300, 70, 500] and cache.free_pages == 40 - 5 - 2 - 8
+    check_codes(cache, plain)
+    kept = cache.evict(turned, 100, 10)
+    for b in range(seqs):
+        got = plain.evict(b, want[b].cpu().numpy(), 100, 10)
+        for h in range(heads):
+            assert kept[b, h, :len(got[h])].tolist() == got[h].tolist()
+    check_codes(cache, plain)
+    assert R.rbd_check() == 0

@@ -256,3 +256,56 @@ def test_a_step_without_rows(launches):
     assert c.attend(rows(0, 4), 4).shape == (0, 512)
     assert c.attend(rows(0, 4), 4, weights=torch.zeros(3, 2, 300)).shape == (0, 512)
     assert c.lens == [64, 0, 6] and launches == ["append", "append", "attn", "attn"]
+
+
+def elements(seqs, heads, w_seq, w_head, cols, at=0):
+    """Element numbers of weights [seqs, heads, cols] with these strides, `at` elements along."""
+    return [at + b * w_seq + h * w_head + t for b in range(seqs) for h in range(heads) for t in range(cols)]
+
+
+def spans(seqs, heads, w_seq, w_head, cols):
+    """One of the strides spans all rows of the other."""
+    if seqs == 1 or heads == 1:
+        return (seqs == 1 or w_seq >= cols) and (heads == 1 or w_head >= cols)
+    return min(w_seq, w_head) >= cols and (w_seq >= (heads - 1) * w_head + cols or w_head >= (seqs - 1) * w_seq + cols)
+
+
+@pytest.mark.parametrize("seqs,heads", [(1, 1), (1, 3), (3, 1), (3, 2), (2, 4)])
+def test_weights_that_share_elements_are_refused(seqs, heads):
+    """Attend writes them and evict cuts them from many blocks at once.  (An accepted call comes as far as the
+    misaligned pointer.)"""
+    lib, cols, base = R.load(), 5, 0x100000
+    c = view(seqs=seqs, heads=heads)
+    attend = lambda w_in, w_out, w_seq, w_head: lib.rbd_kv8_attn(
+        c, FAKE, FAKE, MIS, heads * 128, 4, heads, 1, 0.1, cols, FAKE, heads * 128, base + 4 * w_in, base + 4 * w_out, w_seq,
+        w_head, FAKE, 1 << 40, None)
+    evict = lambda w, w_seq, w_head, width, w_out, o_seq, o_head, width_out, kept=MIS: lib.rbd_kv8_evict(
+        c, FAKE, base + 4 * w, w_seq, w_head, width, 3, 1, FAKE, 1, kept, base + 4 * w_out, o_seq, o_head, width_out, FAKE + 64,
+        None)
+    strides = sorted({0, 1, cols - 1, cols, cols + 1, 2 * cols, 3 * cols, 4 * cols + 3, 40})
+    taken = 0
+    for w_seq in strides:
+        for w_head in strides:
+            if w_head < cols:
+                continue
+            good = spans(seqs, heads, w_seq, w_head, cols)
+            own = elements(seqs, heads, w_seq, w_head, cols)
+            assert not good or len(set(own)) == len(own)
+            assert attend(0, 0, w_seq, w_head) == (3 if good else 1), (w_seq, w_head)
+            assert evict(0, w_seq, w_head, cols, 0, w_seq, w_head, cols) == (3 if good else 1)
+            if not good:
+                # read from one row for all and written elsewhere is fine
+                far = 4000
+                assert evict(0, w_seq, w_head, cols, far, 200, 50, cols) == 3
+                continue
+            taken += 1
+            for shift in range(-3 * (w_seq + w_head) - cols, 3 * (w_seq + w_head) + cols + 1):
+                other = elements(seqs, heads, w_seq, w_head, cols, shift)
+                apart = shift == 0 or not set(own) & set(other)
+                assert attend(4000, 4000 + shift, w_seq, w_head) == (3 if apart else 1), (w_seq, w_head, shift)
+                if shift and set(own) & set(elements(seqs, heads, w_seq, w_head, 3, shift)):
+                    assert evict(4000, w_seq, w_head, cols, 4000 + shift, w_seq, w_head, 3, FAKE) == 1, (w_seq, w_head, shift)
+    assert taken > 3
+    # in place, but with strides of its own
+    if seqs > 1 or heads > 1:
+        assert evict(0, 80, 20, cols, 0, 40, 10, cols, FAKE) == 1
