@@ -571,13 +571,17 @@ __device__ __forceinline__ void kv8_join(const Kv8AttnArgs& a, int64_t slot, int
   if (a.stats && lane == 0) a.stats[fr] = make_float2(m > -INFINITY ? m : 0.f, inv);
 }
 
-// Joins the splits of every (query token, head): a warp each.
+// Joins the splits of every (query token, head): a warp each.  Query tokens are counted through the sequences, as the
+// streaming kernel does: rows of none, and of one whose offsets are refused, stay as they are.
 __global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnArgs a) {
-  const int64_t fr = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (fr >= (int64_t)a.rows * a.q_heads) return;
-  const int64_t tok = fr / a.q_heads;
-  if (tok < __ldg(a.cu) || tok >= __ldg(a.cu + a.seqs)) return;      // rows of no sequence stay as they are
-  kv8_join(a, fr, tok, (int)(fr - tok * a.q_heads));
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t x = at / a.q_heads;
+  if (x >= a.rows) return;
+  Kv8Item it;
+  if (!kv8_find(a.cu, a.lens, a.seqs, a.rows, (int)x, [](int n, int) { return n; }, it)) return;
+  const int64_t tok = it.r0 + it.idx;
+  const int qh = (int)(at - x * a.q_heads);
+  kv8_join(a, tok * a.q_heads + qh, tok, qh);
 }
 
 // weights_out = weights_in + sum of a key's weights over the queries and heads of

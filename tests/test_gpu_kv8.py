@@ -663,3 +663,36 @@ def test_weights_in_any_layout_and_none_that_overlap():
             assert kept[b, h, :len(got[h])].tolist() == got[h].tolist()
     check_codes(cache, plain)
     assert R.rbd_check() == 0
+
+
+@pytest.mark.parametrize("new,held", [(1, 9000), (12, 9000), (300, 9000), (1, 300)])
+def test_rows_of_refused_offsets_are_left_alone(new, held):
+    """Also where the keys are split, whose parts are joined by another kernel."""
+    rng = np.random.default_rng(35)
+    cache, plain = R.Int8KVCache(4, 9216, 1), PlainCache(4, 1, 0)
+    fill(cache, plain, rng, [held, 40, held - 100, 77])
+    rows = 4 * new
+    q = rand(rng, rows, 2)
+    big = 10 ** 6
+    for cu in ([0, new, 2 * new, 3 * new, big], [0, new, big, big, 4 * new], [0, new, 2 * new, -1, 4 * new],
+               [big, big, big, big, big]):
+        work = torch.full((R.rbd_kv8_attn_workspace_bytes(4, 1, 2, rows, 9216, True),), 0x41, dtype=torch.uint8, device="cuda")
+        o = torch.full((rows, 256), 5.0, dtype=torch.bfloat16, device="cuda")
+        w = torch.zeros(4, 1, 9216, device="cuda")
+        R.rbd_kv8_attn(dev(q), torch.tensor(cu, dtype=torch.int32, device="cuda"), cache.device_lens, cache.table, cache.codes,
+                       cache.scales, o, 2, work, 9216, weights_in=w, weights_out=w)
+        assert R.rbd_check() == 1 and R.rbd_check() == 0
+        got = o.float().cpu().numpy().reshape(rows, 2, 128)
+        mine = np.zeros(rows, bool)
+        for b in range(4):
+            gw = w[b].double().cpu().numpy()
+            if 0 <= cu[b] <= cu[b + 1] <= rows:
+                at = slice(cu[b], cu[b + 1])
+                want, dw, eo, ew = plain.attend(b, q[at].astype(np.float64), 2, True)
+                n = plain.len(b)
+                assert (np.abs(got[at] - want) <= eo + 1e-30).all()
+                assert (np.abs(gw[:, :n] - dw) <= ew + 2.0 ** -23 * dw + 1e-30).all() and not gw[:, n:].any()
+                mine[at] = True
+            else:
+                assert not gw.any()
+        assert (got[~mine] == 5).all(), cu
