@@ -176,6 +176,12 @@ __device__ __forceinline__ uint4 eight_codes(const uint2& w) {
   kv8_to_f16<FMT>(FMT == RBD_CODES_INT8 ? prmt(w.y, 0u, 0x3120u) : w.y, h.z, h.w);
   return h;
 }
+// What the softmax takes of a page's scales: the keys' factor, log2 and inverse of the values' one.  A page that the
+// table does not name has zeros for codes and a value scale of zero: all its keys get 2^(0 + log2 0) = 0, and none of
+// that joins L.
+__device__ __forceinline__ float4 page_scales(float2 sc) {
+  return make_float4(sc.x, log2f(sc.y), sc.y > 0.f ? 1.0f / sc.y : 0.f, 0.f);
+}
 // Sixteen codes of one token as fp16, channels 16 c .. 16 c + 15, into an operand tile.
 template <int FMT>
 __device__ __forceinline__ void store_codes(unsigned char* tile, int t, int c, const uint4& w) {
@@ -201,10 +207,10 @@ __global__ void __launch_bounds__(256)
     page[h] = p * kKv8Page < len ? kv8_page(c, b, p) : -1;
   }
   if (threadIdx.x < 2) {
-    float2 sc = make_float2(1.f, 1.f);
+    float2 sc = make_float2(1.f, 0.f);
     if (page[threadIdx.x] >= 0)
       sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page[threadIdx.x], head, 0));
-    a.kv_scale[img * 2 + threadIdx.x] = make_float4(sc.x, log2f(sc.y), 1.0f / sc.y, 0.f);
+    a.kv_scale[img * 2 + threadIdx.x] = page_scales(sc);
   }
   // eight codes a thread and turn: 16 bytes out, whole 128-byte lines a warp
   uint2 raw[16];
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
       reg_dec<104>();
       const int w4 = warp - 12;
       uint4 raw_k[8], raw_v[8];                                  // a step ahead
-      float2 sc = make_float2(1.f, 1.f);
+      float2 sc = make_float2(1.f, 0.f);
       auto fetch = [&](int side, int j, uint4 (&raw)[8]) {
         const int p = (j0 + j) * 2 + (w4 >> 1);
         const int held = len - p * kKv8Page;                     // tokens of the page
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
           if (src && row < held) raw[i] = *reinterpret_cast<const uint4*>(src + kv8_chunk(row, ch));
         }
         if (side == 0) {
-          sc = make_float2(1.f, 1.f);
+          sc = make_float2(1.f, 0.f);
           if (page >= 0) sc = *reinterpret_cast<const float2*>(c.scales + kv8_scale(c, page, head, 0));
         }
       };
@@ -336,8 +342,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
         // Slot j % 4 was last read for step j - 4, whose P V (awaited before its K stage came free for step j - 2)
         // follows that softmax.
         if ((w4 & 1) == 0 && lane == 0)
-          *reinterpret_cast<float4*>(smem + kTlScale + (j & 3) * 32 + (w4 >> 1) * 16) =
-              make_float4(sc.x, log2f(sc.y), 1.0f / sc.y, 0.f);
+          *reinterpret_cast<float4*>(smem + kTlScale + (j & 3) * 32 + (w4 >> 1) * 16) = page_scales(sc);
         if (j + 1 < cnt) fetch(0, j + 1, raw_k);
         fence_async_shared();
         __syncwarp();
@@ -873,9 +878,11 @@ __global__ void __launch_bounds__(kWgThreads, 2)
   if (warp < 8) {
     const int key = k0 + 32 * (warp & 3) + lane;
     float sk = 1.f;
+    bool there = true;                                         // the key's page is one of the pool
     if (key < len) {
       const int page = kv8_page(c, b, key / kKv8Page);
-      if (page >= 0) sk = c.scales[kv8_scale(c, page, head, 0)];
+      there = page >= 0;
+      if (there) sk = c.scales[kv8_scale(c, page, head, 0)];
     }
     const uint64_t sk2 = pack_f32(sk, sk);
     const uint32_t lane_addr = (32u * (uint32_t)(warp & 3)) << 16;
@@ -936,6 +943,7 @@ __global__ void __launch_bounds__(kWgThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_empty[st]);
     }
+    if (!there) acc = 0.f;
     if (warp >= 4) reinterpret_cast<float*>(smem + kWgSum)[tid - 128] = acc;
   }
   tc_fence_before();

@@ -696,3 +696,53 @@ def test_rows_of_refused_offsets_are_left_alone(new, held):
             else:
                 assert not gw.any()
         assert (got[~mine] == 5).all(), cu
+
+
+def check_pages_outside_the_pool(new, held, fmt):
+    """Keys of a page that the table does not name are not there: not for the queries, and not in the key weights."""
+    rng = np.random.default_rng(36)
+    heads, group = 1, 2
+    cache, plain = R.Int8KVCache(3, 9216, heads, pages=450, code_format=fmt), PlainCache(3, heads, fmt)
+    fill(cache, plain, rng, [200, held, 130])
+    counts = [min(new, 200), new, min(new, 130)]
+    rows = sum(counts)
+    q = rand(rng, rows, heads * group)
+    cache.prepare(counts, append=False)
+    first = (held - new) // PAGE                              # pages in front of it are seen whole by every query
+    codes, scales = [list(x) for x in plain.codes[1][0]], [list(x) for x in plain.scales[1][0]]
+    every = list(range(-(-held // PAGE)))
+    for gone, causal in (([0], True), ([first - 1], True), ([1, first // 2 + 1], False), (every[1:], False), (every, True),
+                         (every, False)):
+        table = cache.table.clone()
+        table[1, gone] = torch.tensor([10 ** 6, -1] * len(gone), dtype=torch.int32, device="cuda")[:len(gone)]
+        stay = np.array([t // PAGE not in gone for t in range(held)])
+        for side in range(2):
+            plain.codes[1][0][side] = np.asarray(codes[side], np.float32).reshape(held, 128)[stay]
+            plain.scales[1][0][side] = np.delete(np.asarray(scales[side], np.float32), gone)
+        for weigh in (False, True):
+            need = R.rbd_kv8_attn_workspace_bytes(3, heads, heads * group, rows, 9216, weigh)
+            work = torch.full((need,), 0x41, dtype=torch.uint8, device="cuda")
+            o = torch.full((rows, heads * group * 128), 5.0, dtype=torch.bfloat16, device="cuda")
+            w = torch.from_numpy(rng.random((3, heads, 9216)).astype(np.float32)).cuda() if weigh else None
+            was = w.double().cpu().numpy() if weigh else None
+            R.rbd_kv8_attn(dev(q), cache._cu, cache.device_lens, table, cache.codes, cache.scales, o, heads * group,
+                           work if need else None, 9216, causal=causal, weights_in=w, weights_out=w, code_format=fmt)
+            assert R.rbd_check() == 1 and R.rbd_check() == 0
+            got = o.float().cpu().numpy().reshape(rows, heads * group, 128)
+            at = 0
+            for b, n in enumerate(counts):
+                want, dw, eo, ew = plain.attend(b, q[at:at + n].astype(np.float64), heads * group, causal)
+                assert (np.abs(got[at:at + n] - want) <= eo + 1e-30).all(), (b, gone, causal, weigh)
+                if weigh:
+                    keys = stay if b == 1 else np.ones(cache.lens[b], bool)
+                    add, tol = np.zeros(9216), np.zeros(9216)
+                    add[:keys.size][keys], tol[:keys.size][keys] = dw[0], ew[0]
+                    d = np.abs(w[b, 0].double().cpu().numpy() - (was[b, 0] + add))
+                    assert (d <= tol + 2.0 ** -23 * (was[b, 0] + add) * (add > 0)).all(), (b, gone, causal)
+                at += n
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("new,held", [(70, 400), (300, 9000), (900, 2000)])
+def test_pages_outside_the_pool_many_rows(new, held, fmt):
+    check_pages_outside_the_pool(new, held, fmt)
