@@ -375,16 +375,16 @@ __global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kerne
     }
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      if (a.logits && page >= 0) {
+      if (a.logits) {                                  // (of a page outside the pool: no weight for any query)
+        const int at = (p0 + warp + i * W) * kKv8Page + g;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int rr = 8 * q + 2 * l + x;
           if (rr < nrows) {
             const int r = row_first + rr;
-            float* dst = a.logits + ((int64_t)(r0 + r / a.group) * a.q_heads + head * a.group + r % a.group) * a.logit_ld +
-                         t0 + g;
+            float* dst = a.logits + ((int64_t)(r0 + r / a.group) * a.q_heads + head * a.group + r % a.group) * a.logit_ld + at;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[8 * e] = s[q][e >> 1][2 * (e & 1) + x] * ck[q][x];
+            for (int e = 0; e < 8; ++e) dst[8 * e] = page >= 0 ? s[q][e >> 1][2 * (e & 1) + x] * ck[q][x] : -INFINITY;
           }
         }
       }

@@ -746,3 +746,9 @@ def check_pages_outside_the_pool(new, held, fmt):
 @pytest.mark.parametrize("new,held", [(70, 400), (300, 9000), (900, 2000)])
 def test_pages_outside_the_pool_many_rows(new, held, fmt):
     check_pages_outside_the_pool(new, held, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("new,held", [(1, 400), (12, 400), (1, 9000), (12, 9000)])
+def test_pages_outside_the_pool_few_rows(new, held, fmt):
+    check_pages_outside_the_pool(new, held, fmt)
