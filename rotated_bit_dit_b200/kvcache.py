@@ -252,8 +252,8 @@ class Int8KVCache:
                 raise ValueError("k and v must be bf16 [rows, >= heads * 128], rows contiguous")
             if t.device != self._device:
                 raise ValueError(f"k or v is on {t.device}, the cache on {self._device}")
-            if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
-                raise ValueError("rows of k and v must be 16-byte aligned")
+            if t.data_ptr() % 16 or (t.shape[0] > 1 and (t.stride(0) % 8 or t.stride(0) < self.heads * 128)):
+                raise ValueError("rows of k and v must be 16-byte aligned and must not overlap")
         if counts is not None:
             if k.shape[0] != sum(int(c) for c in counts) or v.shape[0] != k.shape[0]:
                 raise ValueError("counts and rows differ")

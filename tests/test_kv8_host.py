@@ -309,3 +309,18 @@ def test_weights_that_share_elements_are_refused(seqs, heads):
     # in place, but with strides of its own
     if seqs > 1 or heads > 1:
         assert evict(0, 80, 20, cols, 0, 40, 10, cols, FAKE) == 1
+
+
+def test_append_of_overlapping_rows_changes_nothing(launches):
+    """Rows that share memory (expanded, or windows of one buffer) are refused by the entry point: here before the
+    lengths and pages move."""
+    c = R.Int8KVCache(2, 200, 2, pages=7, device="cpu")
+    c.append(rows(100), rows(100), [90, 10])
+    state = (c.lens, list(c._free), [list(p) for p in c._pages])
+    same, windows = rows(1).expand(3, 256), torch.zeros(1024, dtype=torch.bfloat16).as_strided((3, 256), (248, 1))
+    for k, v in ((same, rows(3)), (rows(3), same), (windows, rows(3)), (rows(3), windows)):
+        with pytest.raises(ValueError):
+            c.append(k, v, [2, 1])
+        assert (c.lens, list(c._free), [list(p) for p in c._pages]) == state and check_books(c, 7)
+    c.append(same[:1], windows[:1], [1, 0])              # a single row has no stride
+    assert c.lens == [91, 10]
