@@ -52,13 +52,22 @@ struct Kv8AttnArgs {
   uint8_t* q_image;    // [heads][items][2][32 KB]: the fp16 query tiles (tile kernel), or null
   float* q_rows;       // [heads][items][2][3][128]: score factor, softmax constant and keys seen of every row of them
   uint8_t* kv_image;   // [seqs][image_steps][heads][2][32 KB]: fp16 operands of every 128-key step, or null
-  float4* kv_scale;    // [seqs][image_steps][heads][2]: their page scales (s_k, log2 s_v, 1 / s_v, -)
+  float4* kv_scale;    // [seqs][image_steps][heads][2]: their page scales (s_k, log2 s_v, 1 / s_v, least maximum)
   int image_steps;
 };
 
 namespace {
 
 constexpr float kKv8Lazy = 8.0f;
+// Largest magnitude of a row's maximum m.  A score enters as one fused x - m, with x unrounded and m rounded, so that
+// the largest p is 2^8 at most but for the roundings of m and of log2 s_v - m: below 2^26 they are 2 and 4 at most, and
+// p stays under fp16's 2^16.  A running maximum is not taken lower (p = 0 then, until a score says otherwise).
+constexpr float kKv8Far = 67108864.0f;
+// 1 / L of a row: 0 where it saw no key, NaN where its maximum lies beyond kKv8Far.
+__device__ __forceinline__ float kv8_inverse(float m, float l) {
+  if (m > -INFINITY && !(fabsf(m) < kKv8Far)) return __int_as_float(0x7FFFFFFF);
+  return l == 0.f ? 0.f : 1.0f / l;
+}
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -352,7 +361,7 @@ __global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kerne
         for (int mt = 1; mt < 4; ++mt) mx = fmaxf(mx, fmaxf(s[q][mt][x], s[q][mt][2 + x]));
         mx = col_max(mx);
         ck[q][x] = coef[q][x] * sk;
-        mt_[q][x] = mx > -INFINITY ? fmaf(mx, ck[q][x], lsv) : -INFINITY;
+        mt_[q][x] = mx > -INFINITY ? fmaxf(fmaf(mx, ck[q][x], lsv), -kKv8Far) : -INFINITY;
         move = move || mt_[q][x] > m_run[q][x] + kKv8Lazy;
       }
     }
@@ -507,7 +516,7 @@ __global__ void __launch_bounds__(StreamShape<NQ>::kThreads, 1) kv8_stream_kerne
     const int64_t fr = tok * a.q_heads + qh;
     const float lsum = row_l[rr];
     if (a.nsplit == 1) {
-      const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;
+      const float inv = kv8_inverse(row_m[rr], lsum);
       uint32_t ow[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -564,7 +573,7 @@ __device__ __forceinline__ void kv8_join(const Kv8AttnArgs& a, int64_t slot, int
       acc.w = fmaf(u[i].w, f[i], acc.w);
     }
   }
-  const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;
+  const float inv = kv8_inverse(m, lsum);
   const __nv_bfloat162 p = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), q = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(a.o + tok * a.ldo + (int64_t)qh * kKv8Dim + 4 * lane) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));

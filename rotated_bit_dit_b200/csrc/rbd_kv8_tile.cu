@@ -42,7 +42,7 @@ constexpr int kTlConvThreads = 512;                // with converters
 constexpr uint32_t kTlTile = 32768;                // a 128 x 128 fp16 operand: two 64-channel halves of 128-byte rows
 constexpr uint32_t kTlK = 2 * kTlTile;             // keys, 2 stages
 constexpr uint32_t kTlV = kTlK + 2 * kTlTile;      // values, 2 stages
-constexpr uint32_t kTlScale = kTlV + 2 * kTlTile;  // page scales: 4 slots x 2 pages x (s_k, log2 s_v, 1 / s_v, -)
+constexpr uint32_t kTlScale = kTlV + 2 * kTlTile;  // page scales: 4 slots x 2 pages x (s_k, log2 s_v, 1 / s_v, least maximum)
 constexpr uint32_t kTlCoef = kTlScale + 4 * 32;    // base-2 score factor of the 256 rows
 constexpr uint32_t kTlBar = kTlCoef + 256 * 4;
 constexpr uint32_t kTlSmem = kTlBar + 256 + 1024;  // + alignment slack
@@ -176,11 +176,11 @@ __device__ __forceinline__ uint4 eight_codes(const uint2& w) {
   kv8_to_f16<FMT>(FMT == RBD_CODES_INT8 ? prmt(w.y, 0u, 0x3120u) : w.y, h.z, h.w);
   return h;
 }
-// What the softmax takes of a page's scales: the keys' factor, log2 and inverse of the values' one.  A page that the
-// table does not name has zeros for codes and a value scale of zero: all its keys get 2^(0 + log2 0) = 0, and none of
-// that joins L.
+// What the softmax takes of a page: the keys' factor, log2 and inverse of the values' one, and the least that its
+// maximum counts for.  A page that the table does not name has zeros for codes and a value scale of zero: all its keys
+// get 2^(0 + log2 0) = 0, and none of that joins L.
 __device__ __forceinline__ float4 page_scales(float2 sc) {
-  return make_float4(sc.x, log2f(sc.y), sc.y > 0.f ? 1.0f / sc.y : 0.f, 0.f);
+  return make_float4(sc.x, log2f(sc.y), sc.y > 0.f ? 1.0f / sc.y : 0.f, sc.y > 0.f ? -kKv8Far : -INFINITY);
 }
 // Sixteen codes of one token as fp16, channels 16 c .. 16 c + 15, into an operand tile.
 template <int FMT>
@@ -552,8 +552,8 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
 #pragma unroll
       for (int x = 0; x < 8; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(s[(x >> 2) * 64 + 60 + (x & 3)]));
       const float mx0 = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]), mx1 = max3(fmaxf(mx[4], mx[5]), mx[6], mx[7]);
-      const float mt = fmaxf(mx0 > -INFINITY ? fmaf(mx0, c0, sc0.y) : -INFINITY,
-                             mx1 > -INFINITY ? fmaf(mx1, c1, sc1.y) : -INFINITY);
+      const float mt = fmaxf(mx0 > -INFINITY ? fmaxf(fmaf(mx0, c0, sc0.y), sc0.w) : -INFINITY,
+                             mx1 > -INFINITY ? fmaxf(fmaf(mx1, c1, sc1.y), sc1.w) : -INFINITY);
       const bool move = mt > m_run + kKv8Lazy;
       if (__any_sync(0xffffffffu, move)) {
         const float f = move ? ex2(m_run - mt) : 1.f;
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(CONV ? kTlConvThreads : kTlThreads, 1)
       const int gq = rr % a.group, qh = head * a.group + gq;
       const int64_t tok = r0 + rr / a.group;
       const int64_t fr = tok * a.q_heads + qh;
-      const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
+      const float inv = kv8_inverse(m_run, l_run);
       const bool whole = nsplit == 1;
       const int64_t slot = ((int64_t)(at - a.whole) * 2 * kTlRows + r) * nsplit + split;
       if (live) {

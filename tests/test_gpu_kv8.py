@@ -752,3 +752,76 @@ def test_pages_outside_the_pool_many_rows(new, held, fmt):
 @pytest.mark.parametrize("new,held", [(1, 400), (12, 400), (1, 9000), (12, 9000)])
 def test_pages_outside_the_pool_few_rows(new, held, fmt):
     check_pages_outside_the_pool(new, held, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,held", [(1, 300), (12, 300), (200, 300), (1, 9000), (300, 9000)])
+def test_scores_of_any_size(fmt, n, held):
+    """Scores of +-2^25 and less give the definition's row.  A row whose largest score is beyond 2^27 has no float32
+    maximum to go by and gives NaN; single scores far below a row's largest give their keys no weight.  Other rows
+    are as they were."""
+    rng = np.random.default_rng(37)
+    cache, plain = R.Int8KVCache(1, 9216, 1, code_format=fmt), PlainCache(1, 1, fmt)
+    k, v = rand(rng, held, 1, strong=False), rand(rng, held, 1)
+    k[:, 0, [5, 9, 11]] = 0.0
+    k[64:128, 0, 9] = 2.0 ** 20                              # keys of one page alone answer to channel 9
+    k[70, 0, 11] = 2.0 ** 20                                 # one key to channel 11
+    cache.append(dev(k), dev(v), [held])
+    plain.append(0, k, v)
+    q = rand(rng, n, 2)
+    q[:, :, [5, 9, 11]] = 0.0
+    clean = check_attend(cache, plain, rng, [n], 2, False, q=q)
+    row = n // 2
+    keep = np.ones((n, 2), bool)
+    keep[row] = False
+
+    def attend(a, b):
+        """Row `row` with heads a, b for queries: its outputs and the key weights."""
+        q[row] = np.stack([a, b])
+        w = torch.zeros((1, 1, 9216), device="cuda")
+        got = cache.attend(dev(q), 2, causal=False).float().cpu().numpy().reshape(n, 2, 128)
+        also = cache.attend(dev(q), 2, causal=False, weights=w).float().cpu().numpy().reshape(n, 2, 128)
+        assert R.rbd_check() == 0
+        assert np.array_equal(got[keep], clean[keep]) and np.array_equal(got, also, equal_nan=True)
+        return got[row], w[0, 0, :held].cpu().numpy()
+
+    base, unit = q[row].copy(), np.eye(128, dtype=np.float32)
+    values, own = plain.values(0, 0, 1), plain.values(0, 0, 0)[70, 11]
+    for score in (2.0 ** 10, 2.0 ** 20, 2.0 ** 23, 2.0 ** 24.9):
+        # key 70 takes all the weight: its value, P and its sum rounded alike but for fp16's half step, then bf16
+        x = torch.tensor(score * 128 ** 0.5 / own).bfloat16().float().item()
+        got, w = attend(unit[11] * x, unit[11] * x)
+        assert (np.abs(got - values[70]) <= np.abs(values[70]) * (2.0 ** -8 + 1.01 * 2.0 ** -11) + 1e-30).all(), score
+        # The weight is 2^(x - m) / L from a score formed again: x, its factors, m and m + log2 L are each within half a
+        # step, 2^-24, of at most |x|.
+        off = 2.0 ** (4 * 2.0 ** -24 * (score * 1.4427 + 16)) - 1
+        rows = np.delete(q.reshape(-1, 1, 128).astype(np.float64), [2 * row, 2 * row + 1], 0)
+        _, others, _, ew = plain.attend(0, rows, 1, False)
+        tol = ew[0] + 2.0 ** -20 * (1 + others[0])
+        tol[70] += 2 * off
+        others[0, 70] += 2
+        assert (np.abs(w - others[0]) <= tol).all(), score
+    for x in (2.0 ** 30, 2.0 ** 60, 2.0 ** 120):
+        got, w = attend(unit[11] * x, base[1])               # one score far above the others
+        assert np.isnan(got[0]).all() and np.array_equal(got[1], clean[row, 1]) and np.isnan(w).all()
+    # the page of channel 9 far below the rest: as if it were not there
+    stay = np.ones(held, bool)
+    stay[64:128] = False
+    got, _ = attend(base[0] - unit[9] * 2.0 ** 20, base[1] - unit[9] * 2.0 ** 12)
+    cut = PlainCache(1, 1, fmt)
+    for side in range(2):
+        cut.codes[0][0][side] = plain.codes[0][0][side][stay]
+        cut.scales[0][0][side] = np.delete(plain.scales[0][0][side], 1)
+    want, _, eo, _ = cut.attend(0, base[None].astype(np.float64), 2, False)
+    assert (np.abs(got - want[0]) <= eo[0]).all()
+    # every score far below zero
+    k[:, 0, :] = 0.0
+    k[:, 0, 5] = 2.0 ** 20
+    cache.release(0)
+    cache.append(dev(k), dev(v), [held])
+    cache.prepare([n], append=False)
+    q[:, :, :] = 0.0
+    clean = cache.attend(dev(q), 2, causal=False).float().cpu().numpy().reshape(n, 2, 128)
+    for x in (2.0 ** 30, 2.0 ** 120):
+        got, w = attend(unit[5] * -x, unit[5] * 2.0 ** -20)
+        assert np.isnan(got[0]).all() and np.isfinite(got[1]).all() and np.isnan(w).all()
