@@ -511,9 +511,9 @@ int64_t rbd_kv8_attn_workspace_bytes(int64_t seqs, int64_t heads, int64_t q_head
  * Scores, softmax statistics and sums are float32 on exact products of codes and
  * queries (elements of a query below 2^-32 of its largest are rounded to 2^-40 of
  * that); the softmax's numerators, the value scale inside, are rounded to fp16 for
- * the second product, whose steps end at 2^-24 of the row's largest one.  Scores
- * q k softmax_scale within 2^25 either way are right; a row whose largest one lies
- * beyond 2^26 gives NaN.
+ * the second product, whose steps end at 2^-24 of the row's largest one; one below
+ * 2^-126 of it joins neither sum.  Scores q k softmax_scale within 2^25 either way
+ * are right; a row whose largest one lies beyond 2^26 gives NaN.
  * No result depends on timing.  rows * q_heads <= 2^30.                       */
 rbd_status rbd_kv8_attn(const rbd_kv8* cache, const int32_t* lens, const int32_t* cu, const void* q, int64_t ldq,
                         int64_t rows, int64_t q_heads, int32_t causal, float softmax_scale, int64_t max_len, void* o,

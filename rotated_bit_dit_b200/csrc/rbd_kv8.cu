@@ -203,8 +203,9 @@ __global__ void __launch_bounds__(256)
 // and 10 bits from the top) find the key of the last one to stay and how many of
 // its equals stay with it; then every warp counts and emits its own run of
 // positions, so the kept ones come out in ascending order with no atomics on the
-// output and no dependence on timing.  Short of parallelism rather than bound: 16 x 12
-// blocks over up to 16384 positions take 27 us.
+// output and no dependence on timing.  Bound by its instructions (68% of the issue slots;
+// 192 blocks of 32 warps, one or two an SM): 16 x 12 blocks over up to 16384 positions
+// take 27 us.
 constexpr int kSelThreads = 1024;
 constexpr int kSelBins = 2048;
 constexpr int kSelMaxKeys = 48 * 1024;    // 192 KB of keys; positions beyond are read from global memory

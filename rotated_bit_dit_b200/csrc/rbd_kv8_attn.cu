@@ -14,8 +14,9 @@
 //     O = sum p_t code_t,     L = sum over pages of (sum p_t) / s_v,   o = O / L,
 // because 2^(x_t) code_t s_v = 2^(e_t) code_t and 2^(x_t) = 2^(e_t) / s_v.  The
 // multiplication by s_v costs nothing per element, and p stays in fp16's best
-// range whatever the pages' scales.  p is rounded to fp16 for the second product
-// (a random half step of 2^-11 each); m, L, O and the scores are float32.
+// range whatever the pages' scales (up to 2^126 between them: a p below joins neither
+// sum).  p is rounded to fp16 for the second product (a random half step of 2^-11
+// each, and of 2^-24 below 2^-14); m, L, O and the scores are float32.
 // The maximum moves only when a row exceeds it by 2^8 (p <= 256 then), which
 // leaves most rescales of O out.
 //

@@ -17,15 +17,17 @@
 // Operands come in one of two ways.  Where a key is used by several blocks (prompts,
 // image blocks), kv8_prepare_kernel converts every step's codes once into operand
 // images in the workspace; converting in every block cost the softmax its integer
-// pipe (4096 queries over 16384 keys x 24 heads: 2157 us against 748 without softmax
-// and converters).  Where it is used once, the images' traffic (5 bytes a value
+// pipe (4096 queries over 16384 keys x 24 heads, at an early stage: 2157 us against 748
+// without softmax and converters).  Where it is used once, the images' traffic (5 bytes a value
 // against 1) would dominate, and the block converts for itself.
-// Measured: 4096 queries over 16384 keys x 24 heads in 711 us with the images (47 of
-// it) and the join of what is split (15), 1.16 PFLOP/s, the tensor pipe 63% busy.  What bounds it is the chain of a query
-// tile: a softmax step (128 scores a thread, about 2000 cycles, 1275 of them
-// exponentials) and then its P.V and Q.K^T (1024), of which the other tile hides the
-// latter; of a ragged causal prompt (21186 tokens x 48 heads: 971 us, 0.88 PFLOP/s)
-// also setting up and leaving a block, some 14000 of 75000 cycles.
+// Measured: 4096 queries over 16384 keys x 24 heads with the images (47 us of it) and
+// the join of what is split (15) in 705 us, 1.17 PFLOP/s, where something else runs
+// between the calls, and 785 us, 1.05 PFLOP/s, call after call under the power cap; the
+// tensor pipe is 63% busy.  What bounds it is the chain of a query tile: a softmax step
+// (128 scores a thread, about 2000 cycles, 1275 of them exponentials) and then its P.V
+// and Q.K^T (1024), of which the other tile hides the latter; of ragged causal prompts
+// (21186 tokens x 48 heads: 1011 and 1030 us, 0.84 PFLOP/s) also setting up and leaving
+// a block, some 14000 of 75000 cycles.
 #include <type_traits>
 
 #include "rbd_kv8.cuh"
@@ -70,7 +72,8 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 // 2^x and is the longest phase of the softmax (1590 cycles of a 128-key step without this, 1275 with; 960 -> 922 us
 // at 4096 queries over 16384 keys x 24 heads; half of the keys: 985 us).  x = n + f with n the nearest whole number
 // and |f| <= 1/2; 2^f by its degree-4 polynomial of least largest relative error (2.6e-6, far under P's half step of
-// 2^-11); n added to the exponent.
+// 2^-11); n added to the exponent.  A NaN comes out as a number: a row has one from a query that is not finite alone,
+// and then in every key, so that the other three quarters keep it.
 __device__ __forceinline__ void ex2_poly(float& x, float& y) {
   const uint64_t v = pack_f32(fmaxf(x, -126.f), fmaxf(y, -126.f));
   const uint64_t t = add_f32x2(v, pack_f32(12582912.f, 12582912.f));               // 1.5 * 2^23: rounds to whole
@@ -708,8 +711,8 @@ __global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const Kv8AttnArgs
 // SM, so that one sums while the other waits.  Under a causal mask the first keys see
 // every tile and the last ones one: with few blocks the tiles of each are cut into
 // `parts`, whose sums kv8_weigh_add_kernel adds in order.
-// Measured: two causal prompts of 3001 and 1954 tokens, 48 heads in groups of 4: 150 us
-// for this pass, of 383 with the attention; about six blocks an SM, half or twice as
+// Measured: two causal prompts of 3001 and 1954 tokens, 48 heads in groups of 4: 155 us
+// for this pass, of 380 with the attention; about six blocks an SM, half or twice as
 // many being 1 to 3% slower, and a polynomial for part of the exponentials no faster.
 //   warps 0-3, 4-7  sums, query tiles in turn;  warp 8  producer;  warp 9  TMEM owner and MMA issuer.
 namespace {
@@ -1021,7 +1024,8 @@ Kv8Plan kv8_plan(int seqs, int heads, int q_heads, int rows, int max_len, bool w
     // Blocks of the tile kernel that last alike (where a sequence's queries are few beside its keys) run in waves.
     // Those of a last, partly filled wave are split when that is shorter by an estimate in steps: a block's setup
     // counts as four, the join as two and 1/32 for every split (4096 queries over 16384 keys x 24 heads, 384 blocks:
-    // 756 us whole, 711 with the last 88 split in three; 1024 queries, 96 blocks: 294 us whole, 261 split in three).
+    // 739 us whole, 705 with the last 88 split in three; 1024 queries, 96 blocks: 290-320 us whole, 262-275 split in
+    // three).
     const int tail = (int)(blocks % 148);
     int64_t best = 32 * (int64_t)(steps + 4);
     for (int k = 2; tail > 0 && k <= std::min(64, steps / 8); ++k) {

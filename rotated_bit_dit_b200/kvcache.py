@@ -268,8 +268,9 @@ class Int8KVCache:
                weights_out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Attention of the prepared rows' queries (bf16 [rows, >= heads*128], heads a multiple of the cache's)
         over the tokens held; causal: a sequence's queries are its last tokens.  A query that sees nothing gets
-        zeros.  weights: float32 [sequences, cache heads, >= max_tokens], to which every key's weight is added (into
-        weights_out when given).  Returns bf16 [rows, heads*128] (out)."""
+        zeros, one with an infinite or NaN element NaN.  weights: float32 [sequences, cache heads, >= max_tokens] whose
+        rows share no element, to which every key's weight is added (into weights_out when given: of the same strides,
+        apart from it).  Returns bf16 [rows, heads*128] (out)."""
         self._prepared(q.shape[0])
         if heads <= 0 or heads % self.heads:
             raise ValueError("heads must be a multiple of the cache's heads")
@@ -374,7 +375,8 @@ class Int8KVCache:
         return kept
 
     def release(self, sequence: int) -> None:
-        """Empty a sequence; its pages go back to the pool.  Afterwards prepare() again."""
+        """Empty a sequence; its pages go back to the pool.  Weights that attend() added up for it are the caller's to
+        clear.  Afterwards prepare() again."""
         self._not_captured()
         if not 0 <= sequence < self.sequences:
             raise ValueError("no such sequence")
